@@ -47,6 +47,9 @@ EXPORTED = (
     "bimamba_ssd_fwd_rev_backward",
     "bimamba_in_proj",
     "bimamba_out_proj",
+    "bimamba_layer_norm",
+    "bimamba_layer_norm_backward_workspace_bytes",
+    "bimamba_layer_norm_backward",
     "bimamba_noalloc_scratch_bytes",
     "bimamba_block_decode_noalloc",
 )
@@ -108,6 +111,13 @@ def _load() -> ctypes.CDLL:
     lib.bimamba_in_proj.argtypes = [i, i, i, i, i, vp, vp, vp, vp, vp, vp]
     lib.bimamba_out_proj.restype = i
     lib.bimamba_out_proj.argtypes = [i, i, i, vp, vp, vp, vp]
+    ll, f = ctypes.c_longlong, ctypes.c_float
+    lib.bimamba_layer_norm.restype = i
+    lib.bimamba_layer_norm.argtypes = [ll, i, vp, vp, vp, vp, f, vp, vp, vp, vp, i, vp]
+    lib.bimamba_layer_norm_backward_workspace_bytes.restype = sz
+    lib.bimamba_layer_norm_backward_workspace_bytes.argtypes = [ll, i]
+    lib.bimamba_layer_norm_backward.restype = i
+    lib.bimamba_layer_norm_backward.argtypes = [ll, i] + [vp] * 9 + [i, vp, sz, vp]
     lib.bimamba_noalloc_scratch_bytes.restype = sz
     lib.bimamba_noalloc_scratch_bytes.argtypes = []
     lib.bimamba_block_decode_noalloc.restype = i
@@ -361,6 +371,99 @@ def bimamba_out_proj(y, w_out, out, stream=None):
                                _ptr(out), _stream(stream))
     _check(st, "bimamba_out_proj")
     return out
+
+
+class _Args:
+    """The tensors of one call: each has to be a dense CUDA tensor of the
+    given type and shape, on one device, which is made current for the call
+    (the kernels launch there, on that device's current stream unless one is
+    given)."""
+
+    def __init__(self, where: str, lead: torch.Tensor, stream):
+        self.where, self.dev, self._stream = where, lead.device, stream
+        if lead.device.type != "cuda":
+            self.bad(f"a CUDA tensor is wanted, got one on {lead.device}")
+
+    def bad(self, why: str):
+        raise BimambaError(BIMAMBA_ERR_INVALID, f"{self.where}: {why}")
+
+    def ptr(self, name: str, t, dtype, shape) -> int:
+        if t.dtype is not dtype or t.shape != shape or t.device != self.dev or not t.is_contiguous():
+            self.bad(f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on {self.dev} is wanted, got "
+                     f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+        return t.data_ptr()
+
+    def opt(self, name: str, t, dtype, shape):
+        return None if t is None else self.ptr(name, t, dtype, shape)
+
+    def workspace(self, t):
+        if t is None:
+            return None, 0
+        if t.device != self.dev or not t.is_contiguous():
+            self.bad(f"workspace: a dense tensor on {self.dev} is wanted")
+        return t.data_ptr(), t.numel() * t.element_size()
+
+    def call(self, fn, *args):
+        index = self.dev.index
+        here = torch.cuda.current_device()
+        if here == index:
+            st = fn(*args, self._raw_stream(index))
+        else:
+            with torch.cuda.device(index):
+                st = fn(*args, self._raw_stream(index))
+        if st != BIMAMBA_OK:
+            raise BimambaError(st, self.where)
+
+    def _raw_stream(self, index):
+        s = self._stream
+        if s is None:
+            return torch.cuda.current_stream(index).cuda_stream
+        return s if isinstance(s, int) else s.cuda_stream
+
+
+def bimamba_layer_norm(x, gamma, beta, y, mean, rstd, *, residual=None, sum_out=None, eps=1e-5,
+                       stream=None):
+    """y = layer norm of x (+ residual) over the last dimension, gamma/beta
+    (beta may be None) fp32; mean and rstd (one fp32 value a row) and, with a
+    residual, sum_out = x + residual are written for the backward pass."""
+    a = _Args("bimamba_layer_norm", x, stream)
+    code, td, cols = _dtype_code(x), x.dtype, x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    f32, vec = torch.float32, (cols,)
+    a.call(_lib.bimamba_layer_norm, rows, cols, a.ptr("x", x, td, x.shape),
+           a.opt("residual", residual, td, x.shape), a.ptr("gamma", gamma, f32, vec),
+           a.opt("beta", beta, f32, vec), eps, a.ptr("y", y, td, x.shape),
+           a.opt("sum_out", sum_out, td, x.shape), a.ptr("mean", mean, f32, x.shape[:-1]),
+           a.ptr("rstd", rstd, f32, x.shape[:-1]), code)
+    return y
+
+
+def bimamba_layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_lib.bimamba_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+def new_layer_norm_workspace(x) -> torch.Tensor:
+    """Workspace for bimamba_layer_norm_backward over rows like x's."""
+    cols = x.shape[-1]
+    n = bimamba_layer_norm_backward_workspace_bytes(x.numel() // cols if cols else 0, cols)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=x.device)
+
+
+def bimamba_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dgamma, dbeta, workspace, *, dsum=None,
+                                stream=None):
+    """Gradients of the layer norm from dy (and dsum, the gradient that
+    reaches h past the norm): writes dx, dgamma and, unless None, dbeta.
+    h is the forward call's x, or its sum_out where it had a residual."""
+    a = _Args("bimamba_layer_norm_backward", h, stream)
+    code, td, cols = _dtype_code(h), h.dtype, h.shape[-1]
+    rows = h.numel() // cols if cols else 0
+    f32, vec, each = torch.float32, (cols,), h.shape[:-1]
+    ws, ws_bytes = a.workspace(workspace)
+    a.call(_lib.bimamba_layer_norm_backward, rows, cols, a.ptr("dy", dy, td, h.shape),
+           a.ptr("h", h, td, h.shape), a.ptr("gamma", gamma, f32, vec), a.ptr("mean", mean, f32, each),
+           a.ptr("rstd", rstd, f32, each), a.opt("dsum", dsum, td, h.shape), a.ptr("dx", dx, td, h.shape),
+           a.ptr("dgamma", dgamma, f32, vec), a.opt("dbeta", dbeta, f32, vec), code, ws, ws_bytes)
+    return dx
 
 
 def bimamba_noalloc_scratch_bytes() -> int:

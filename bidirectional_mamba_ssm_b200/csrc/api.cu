@@ -64,6 +64,26 @@ static int check_dims(const bimamba_dims *d)
     return BIMAMBA_OK;
 }
 
+// Whether [a, a + an) and [b, b + bn) share a byte (null ranges share none).
+static bool overlap(const void *a, size_t an, const void *b, size_t bn)
+{
+    const char *p = static_cast<const char *>(a), *q = static_cast<const char *>(b);
+    return p && q && p < q + bn && q < p + an;
+}
+
+// Whether any of the `nout` first ranges overlaps another of the `n`.
+struct Range {
+    const void *p;
+    size_t bytes;
+};
+static bool any_output_overlaps(const Range *r, int nout, int n)
+{
+    for (int i = 0; i < nout; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes)) return true;
+    return false;
+}
+
 static int cuda_status(cudaError_t e) { return e == cudaSuccess ? BIMAMBA_OK : BIMAMBA_ERR_CUDA; }
 
 int check_block_decode(const bimamba_dims *d, const void *xbc_block, const void *dt_block,
@@ -512,6 +532,67 @@ int bimamba_ssd_fwd_rev_backward(const bimamba_dims *d, const void *xbc, const v
     q.dinit = dinit;
     q.workspace = workspace;
     return cuda_status(launch_backward(q, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static int check_norm(long long rows, int cols, int dtype)
+{
+    if (rows < 0 || cols <= 0) return BIMAMBA_ERR_INVALID;
+    if (dtype != BIMAMBA_F32 && dtype != BIMAMBA_BF16) return BIMAMBA_ERR_INVALID;
+    return layer_norm_supported(rows, cols) ? BIMAMBA_OK : BIMAMBA_ERR_UNSUPPORTED;
+}
+
+int bimamba_layer_norm(long long rows, int cols, const void *x, const void *residual,
+                       const float *gamma, const float *beta, float eps, void *y, void *sum_out,
+                       float *mean, float *rstd, int dtype, bimamba_stream_t stream)
+{
+    const int st = check_norm(rows, cols, dtype);
+    if (st != BIMAMBA_OK) return st;
+    if (!(eps >= 0.0f)) return BIMAMBA_ERR_INVALID;
+    if ((residual != nullptr) != (sum_out != nullptr)) return BIMAMBA_ERR_INVALID;
+    if (rows == 0) return BIMAMBA_OK;
+    if (!x || !gamma || !y || !mean || !rstd) return BIMAMBA_ERR_INVALID;
+    const size_t nx = (size_t)rows * cols * (dtype == BIMAMBA_F32 ? 4 : 2), nr = (size_t)rows * 4,
+                 nc = (size_t)cols * 4;
+    const Range r[] = {{y, nx}, {sum_out, nx}, {mean, nr}, {rstd, nr},
+                       {x, nx}, {residual, nx}, {gamma, nc}, {beta, nc}};
+    for (const Range &q : r)
+        if (q.p && !aligned16(q.p)) return BIMAMBA_ERR_INVALID;
+    if (any_output_overlaps(r, 4, 8)) return BIMAMBA_ERR_INVALID;
+    const NormProblem q{rows, cols, x, residual, gamma, beta, eps, y, sum_out, mean, rstd};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == BIMAMBA_F32 ? launch_layer_norm<float>(q, s)
+                                            : launch_layer_norm<__nv_bfloat16>(q, s));
+}
+
+size_t bimamba_layer_norm_backward_workspace_bytes(long long rows, int cols)
+{
+    if (check_norm(rows, cols, BIMAMBA_F32) != BIMAMBA_OK) return 0;
+    return layer_norm_backward_ws_bytes(rows, cols);
+}
+
+int bimamba_layer_norm_backward(long long rows, int cols, const void *dy, const void *h,
+                                const float *gamma, const float *mean, const float *rstd,
+                                const void *dsum, void *dx, float *dgamma, float *dbeta, int dtype,
+                                void *workspace, size_t workspace_bytes, bimamba_stream_t stream)
+{
+    const int st = check_norm(rows, cols, dtype);
+    if (st != BIMAMBA_OK) return st;
+    if (!gamma || !dgamma) return BIMAMBA_ERR_INVALID;
+    if (rows > 0 && (!dy || !h || !mean || !rstd || !dx)) return BIMAMBA_ERR_INVALID;
+    const size_t nx = (size_t)rows * cols * (dtype == BIMAMBA_F32 ? 4 : 2), nr = (size_t)rows * 4,
+                 nc = (size_t)cols * 4;
+    const size_t need = layer_norm_backward_ws_bytes(rows, cols);
+    const Range r[] = {{dx, nx}, {dgamma, nc}, {dbeta, nc}, {workspace, need}, {dy, nx}, {h, nx},
+                       {gamma, nc}, {mean, nr}, {rstd, nr}, {dsum, nx}};
+    for (const Range &q : r)
+        if (q.p && q.p != workspace && !aligned16(q.p)) return BIMAMBA_ERR_INVALID;
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return BIMAMBA_ERR_WORKSPACE;
+    if (any_output_overlaps(r, 4, 10)) return BIMAMBA_ERR_INVALID;
+    const NormBackwardProblem q{rows, cols, dy, h, dsum, gamma, mean, rstd, dx, dgamma, dbeta, workspace};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == BIMAMBA_F32 ? launch_layer_norm_backward<float>(q, s)
+                                            : launch_layer_norm_backward<__nv_bfloat16>(q, s));
 }
 
 }  // extern "C"

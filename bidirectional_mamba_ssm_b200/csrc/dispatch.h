@@ -127,6 +127,32 @@ bool backward_tc_supported(const bimamba_dims &d);
 size_t backward_tc_state_bytes(const bimamba_dims &d);
 cudaError_t launch_backward_tc(const BackwardTcProblem &q, cudaStream_t stream);
 
+// (residual add and) layer norm, and its backward pass
+struct NormProblem {
+    long long rows;
+    int cols;
+    const void *x, *residual;   // residual (and sum_out) may be null
+    const float *gamma, *beta;  // beta may be null
+    float eps;
+    void *y, *sum_out;
+    float *mean, *rstd;
+};
+struct NormBackwardProblem {
+    long long rows;
+    int cols;
+    const void *dy, *h, *dsum;  // dsum may be null
+    const float *gamma, *mean, *rstd;
+    void *dx;
+    float *dgamma, *dbeta;      // dbeta may be null
+    void *workspace;            // layer_norm_backward_ws_bytes
+};
+bool layer_norm_supported(long long rows, int cols);
+size_t layer_norm_backward_ws_bytes(long long rows, int cols);
+template <typename T>
+cudaError_t launch_layer_norm(const NormProblem &q, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_layer_norm_backward(const NormBackwardProblem &q, cudaStream_t stream);
+
 template <typename T>
 cudaError_t launch_conv_silu(const void *u, void *out, const float *w, const float *bias,
                              const void *tail, int batch, int len, int ch, int rev, int silu,

@@ -1,0 +1,453 @@
+// norm.cu -- the (residual add and) layer norm in front of a mixer's input
+// projection, and its backward pass.
+//
+// Operation ("DiffuMamba" blog post, network-architecture listing: mixer
+// blocks with a LayerNorm; eps inside the root, biased variance), per row:
+//     h = x + r            (r optional; h kept in fp32, stored rounded once)
+//     m = mean(h),  s = 1 / sqrt(mean((h - m)^2) + eps)
+//     y = (h - m) s g + b
+// and, with z = (h - m) s and a = dy g,
+//     dx = s (a - mean(a) - z mean(a z)) + dsum
+//     dg = sum over rows of dy z,   db = sum over rows of dy.
+//
+// Bound by HBM: every activation is read or written once, everything else
+// stays in registers.  A row belongs to `kWarps` warps, each thread holding
+// `kVec` 16-byte-per-8-element vectors of it.
+#include "common.cuh"
+#include "dispatch.h"
+
+namespace bimamba {
+
+namespace {
+
+// 8 consecutive elements as loaded (bf16: 16 bytes, fp32: 32 bytes).
+template <typename T> struct Raw8 {
+    uint4 r[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(r[i].x);
+                v[4 * i + 1] = __uint_as_float(r[i].y);
+                v[4 * i + 2] = __uint_as_float(r[i].z);
+                v[4 * i + 3] = __uint_as_float(r[i].w);
+            }
+        } else {
+            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r[0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __bfloat1622float2(h[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Barrier over the warps of one row (rows of a CTA advance independently).
+template <int kWarps> __device__ __forceinline__ void row_sync(int slot)
+{
+    if constexpr (kWarps > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(32 * kWarps) : "memory");
+}
+
+constexpr int kNormThreads = 256;
+constexpr int norm_threads(int warps) { return warps * 32 > kNormThreads ? warps * 32 : kNormThreads; }
+
+constexpr int kFwdVec = 4;   // vectors a thread holds in the forward pass
+constexpr int kBwdVec = 2;   // in the backward pass (which also keeps column sums)
+
+}  // namespace
+
+// Forward: one row per `kWarps` warps.  Mean and squared deviations are
+// formed per warp in two passes over its registers and merged across the
+// row's warps (counts n_w, means m_w, deviations d_w):
+//     m = sum n_w m_w / n,   var n = sum d_w + n_w (m_w - m)^2
+// so one exchange through shared memory suffices and nothing cancels.
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(norm_threads(kWarps))
+layer_norm_kernel(const T *__restrict__ x, const T *__restrict__ residual, const float *__restrict__ gamma,
+                  const float *__restrict__ beta, T *__restrict__ y, T *__restrict__ sum_out,
+                  float *__restrict__ mean_out, float *__restrict__ rstd_out, long long rows, int cols, float eps)
+{
+    constexpr int kRows = norm_threads(kWarps) / (32 * kWarps);
+    __shared__ float2 part[kRows][kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = warp / kWarps, rw = warp % kWarps;
+    const long long row = (long long)blockIdx.x * kRows + slot;
+    if (row >= rows) return;   // (a whole row's warps leave together)
+    const int vecs = cols >> 3;
+    const int v0 = rw * 32 + lane;   // this thread's vectors: v0 + 32 kWarps i
+    const T *xr = x + row * cols;
+    const T *rr = residual ? residual + row * cols : nullptr;
+
+    float v[kFwdVec][8];
+    {
+        Raw8<T> a[kFwdVec], b[kFwdVec];
+#pragma unroll
+        for (int i = 0; i < kFwdVec; ++i) {
+            const int e = v0 + 32 * kWarps * i;
+            if (e < vecs) a[i].load(xr + 8 * e);
+        }
+        if (rr) {
+#pragma unroll
+            for (int i = 0; i < kFwdVec; ++i) {
+                const int e = v0 + 32 * kWarps * i;
+                if (e < vecs) b[i].load(rr + 8 * e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFwdVec; ++i) {
+            const int e = v0 + 32 * kWarps * i;
+            if (e >= vecs) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+                continue;
+            }
+            a[i].get(v[i]);
+            if (rr) {
+                float w[8];
+                b[i].get(w);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[i][q] += w[q];
+                Vec8<T>::store(sum_out + row * cols + 8 * e, v[i]);
+            }
+        }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kFwdVec; ++i)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += v[i][q];
+    s = warp_sum(s);
+    // elements of warp w: its full strides, and what is left of the last one
+    auto count = [&](int w) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kFwdVec; ++i) n += min(max(vecs - 32 * (w + kWarps * i), 0), 32);
+        return 8.0f * n;
+    };
+    const float nw = count(rw);
+    float mean = nw > 0.0f ? s / nw : 0.0f;
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kFwdVec; ++i) {
+        if (v0 + 32 * kWarps * i < vecs) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) d = fmaf(v[i][q] - mean, v[i][q] - mean, d);
+        }
+    }
+    d = warp_sum(d);
+    if constexpr (kWarps > 1) {
+        if (lane == 0) part[slot][rw] = make_float2(mean, d);
+        row_sync<kWarps>(slot);
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaf(count(w), part[slot][w].x, m);
+        m /= (float)cols;
+        d = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 q = part[slot][w];
+            d += fmaf(count(w) * (q.x - m), q.x - m, q.y);
+        }
+        mean = m;
+    }
+    const float rstd = rsqrtf(d / (float)cols + eps);
+    if (rw == 0 && lane == 0) {
+        mean_out[row] = mean;
+        rstd_out[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < kFwdVec; ++i) {
+        const int e = v0 + 32 * kWarps * i;
+        if (e >= vecs) continue;
+        float g[8], o[8];
+        Vec8<float>::load(gamma + 8 * e, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = (v[i][q] - mean) * rstd * g[q];
+        if (beta) {
+            Vec8<float>::load(beta + 8 * e, g);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] += g[q];
+        }
+        Vec8<T>::store(y + row * cols + 8 * e, o);
+    }
+}
+
+// Backward: a fixed set of rows per group of `kWarps` warps, so that each
+// thread keeps its own columns of dg and db in registers over all of them;
+// the CTA's groups join in shared memory and write one partial row
+// part[cta][dg | db][cols].  The order of every sum is fixed by the launch.
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(norm_threads(kWarps))
+layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const float *__restrict__ gamma,
+                      const float *__restrict__ mean, const float *__restrict__ rstd, const T *__restrict__ dsum,
+                      T *__restrict__ dx, float *__restrict__ part, long long rows, int cols)
+{
+    constexpr int kRows = norm_threads(kWarps) / (32 * kWarps);
+    __shared__ float2 red[2][kRows][kWarps];
+    extern __shared__ float joined[];   // [kRows - 1][2][cols]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = warp / kWarps, rw = warp % kWarps;
+    const int vecs = cols >> 3;
+    const int v0 = rw * 32 + lane;
+    const float inv_cols = 1.0f / (float)cols;
+
+    float g[kBwdVec][8], dg[kBwdVec][8], db[kBwdVec][8];
+#pragma unroll
+    for (int i = 0; i < kBwdVec; ++i) {
+        const int e = v0 + 32 * kWarps * i;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) g[i][q] = dg[i][q] = db[i][q] = 0.0f;
+        if (e < vecs) Vec8<float>::load(gamma + 8 * e, g[i]);
+    }
+    Raw8<T> rh[kBwdVec], rd[kBwdVec], rs[kBwdVec];
+    float m = 0.0f, s = 0.0f;
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < kBwdVec; ++i) {
+            const int e = v0 + 32 * kWarps * i;
+            if (e < vecs) {
+                rh[i].load(h + row * cols + 8 * e);
+                rd[i].load(dy + row * cols + 8 * e);
+                if (dsum) rs[i].load(dsum + row * cols + 8 * e);
+            }
+        }
+        m = mean[row];
+        s = rstd[row];
+    };
+    const long long stride = (long long)gridDim.x * kRows;
+    long long row = (long long)blockIdx.x * kRows + slot;
+    if (row < rows) fetch(row);
+    for (int it = 0; row < rows; row += stride, it ^= 1) {
+        float z[kBwdVec][8], a[kBwdVec][8], sv[kBwdVec][8];
+        const float rs_row = s;
+        float sa = 0.0f, saz = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kBwdVec; ++i) {
+            const bool in = v0 + 32 * kWarps * i < vecs;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) z[i][q] = a[i][q] = sv[i][q] = 0.0f;
+            if (!in) continue;
+            rh[i].get(z[i]);
+            rd[i].get(a[i]);
+            if (dsum) rs[i].get(sv[i]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                z[i][q] = (z[i][q] - m) * s;
+                dg[i][q] = fmaf(a[i][q], z[i][q], dg[i][q]);
+                db[i][q] += a[i][q];
+                a[i][q] *= g[i][q];
+                sa += a[i][q];
+                saz = fmaf(a[i][q], z[i][q], saz);
+            }
+        }
+        if (row + stride < rows) fetch(row + stride);   // the next row's loads run under this row's sums
+        sa = warp_sum(sa);
+        saz = warp_sum(saz);
+        if constexpr (kWarps > 1) {
+            // (two buffers: a warp may be one row ahead of the slowest reader)
+            if (lane == 0) red[it][slot][rw] = make_float2(sa, saz);
+            row_sync<kWarps>(slot);
+            sa = saz = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 q = red[it][slot][w];
+                sa += q.x;
+                saz += q.y;
+            }
+        }
+        sa *= inv_cols;
+        saz *= inv_cols;
+#pragma unroll
+        for (int i = 0; i < kBwdVec; ++i) {
+            const int e = v0 + 32 * kWarps * i;
+            if (e >= vecs) continue;
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = fmaf(rs_row, a[i][q] - sa - z[i][q] * saz, sv[i][q]);
+            Vec8<T>::store(dx + row * cols + 8 * e, o);
+        }
+    }
+    if constexpr (kRows > 1) {
+        if (slot > 0) {
+            float *j = joined + (size_t)(slot - 1) * 2 * cols;
+#pragma unroll
+            for (int i = 0; i < kBwdVec; ++i) {
+                const int e = v0 + 32 * kWarps * i;
+                if (e < vecs) {
+                    Vec8<float>::store(j + 8 * e, dg[i]);
+                    Vec8<float>::store(j + cols + 8 * e, db[i]);
+                }
+            }
+        }
+        __syncthreads();
+        if (slot > 0) return;
+        for (int k = 0; k < kRows - 1; ++k) {
+            const float *j = joined + (size_t)k * 2 * cols;
+#pragma unroll
+            for (int i = 0; i < kBwdVec; ++i) {
+                const int e = v0 + 32 * kWarps * i;
+                if (e >= vecs) continue;
+                float t[8];
+                Vec8<float>::load(j + 8 * e, t);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) dg[i][q] += t[q];
+                Vec8<float>::load(j + cols + 8 * e, t);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) db[i][q] += t[q];
+            }
+        }
+    }
+    float *out = part + (size_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int i = 0; i < kBwdVec; ++i) {
+        const int e = v0 + 32 * kWarps * i;
+        if (e < vecs) {
+            Vec8<float>::store(out + 8 * e, dg[i]);
+            Vec8<float>::store(out + cols + 8 * e, db[i]);
+        }
+    }
+}
+
+// dg / db = sum over the partial rows.  A CTA owns 32 columns; its 16 warps
+// take every 16th partial row, then join in order.
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(32 * kJoinWarps)
+layer_norm_join_kernel(const float *__restrict__ part, float *__restrict__ dgamma, float *__restrict__ dbeta,
+                       int nparts, int cols)
+{
+    __shared__ float sums[kJoinWarps][33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * 32 + lane;
+    const int which = blockIdx.y;   // 0: dgamma, 1: dbeta
+    float acc = 0.0f;
+    if (c < cols) {
+        const float *p = part + (size_t)which * cols + c;
+#pragma unroll 8
+        for (int r = warp; r < nparts; r += kJoinWarps) acc += p[(size_t)r * 2 * cols];
+    }
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+        acc = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) acc += sums[w][lane];
+        (which ? dbeta : dgamma)[c] = acc;
+    }
+}
+
+namespace {
+
+// Warps per row: the fewest (a power of two) that hold the row at `vec`
+// vectors a thread.
+int warps_per_row(int cols, int vec)
+{
+    int w = 1;
+    while (w * 32 * vec * 8 < cols) w *= 2;
+    return w;
+}
+
+constexpr int kBwdCtas = 2 * 148;   // two CTAs per SM
+
+int bwd_ctas(long long rows, int cols)
+{
+    const int w = warps_per_row(cols, kBwdVec);
+    const int per = norm_threads(w) / (32 * w);
+    const long long need = (rows + per - 1) / per;
+    return (int)(need < kBwdCtas ? need : kBwdCtas);
+}
+
+template <typename T, int kWarps>
+cudaError_t launch_fwd(const NormProblem &q, cudaStream_t stream)
+{
+    constexpr int kRows = norm_threads(kWarps) / (32 * kWarps);
+    const long long ctas = (q.rows + kRows - 1) / kRows;
+    layer_norm_kernel<T, kWarps><<<(unsigned)ctas, norm_threads(kWarps), 0, stream>>>(
+        static_cast<const T *>(q.x), static_cast<const T *>(q.residual), q.gamma, q.beta, static_cast<T *>(q.y),
+        static_cast<T *>(q.sum_out), q.mean, q.rstd, q.rows, q.cols, q.eps);
+    return cudaGetLastError();
+}
+
+template <typename T, int kWarps>
+cudaError_t launch_bwd(const NormBackwardProblem &q, cudaStream_t stream)
+{
+    constexpr int kRows = norm_threads(kWarps) / (32 * kWarps);
+    const int ctas = bwd_ctas(q.rows, q.cols);
+    const size_t smem = (size_t)(kRows - 1) * 2 * q.cols * sizeof(float);
+    float *part = static_cast<float *>(q.workspace);
+    if (ctas > 0) {   // (no rows: the sums are empty)
+        layer_norm_bwd_kernel<T, kWarps><<<ctas, norm_threads(kWarps), smem, stream>>>(
+            static_cast<const T *>(q.dy), static_cast<const T *>(q.h), q.gamma, q.mean, q.rstd,
+            static_cast<const T *>(q.dsum), static_cast<T *>(q.dx), part, q.rows, q.cols);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        count_launch();
+    }
+    layer_norm_join_kernel<<<dim3((q.cols + 31) / 32, q.dbeta ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(
+        part, q.dgamma, q.dbeta, ctas, q.cols);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool layer_norm_supported(long long rows, int cols)
+{
+    return cols % 8 == 0 && cols <= 8192 && rows <= (1ll << 31) - 1;
+}
+
+size_t layer_norm_backward_ws_bytes(long long rows, int cols)
+{
+    return (size_t)bwd_ctas(rows, cols) * 2 * cols * sizeof(float);
+}
+
+template <typename T>
+cudaError_t launch_layer_norm(const NormProblem &q, cudaStream_t stream)
+{
+    cudaError_t e;
+    switch (warps_per_row(q.cols, kFwdVec)) {
+    case 1: e = launch_fwd<T, 1>(q, stream); break;
+    case 2: e = launch_fwd<T, 2>(q, stream); break;
+    case 4: e = launch_fwd<T, 4>(q, stream); break;
+    default: e = launch_fwd<T, 8>(q, stream); break;
+    }
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_layer_norm_backward(const NormBackwardProblem &q, cudaStream_t stream)
+{
+    cudaError_t e;
+    switch (warps_per_row(q.cols, kBwdVec)) {
+    case 1: e = launch_bwd<T, 1>(q, stream); break;
+    case 2: e = launch_bwd<T, 2>(q, stream); break;
+    case 4: e = launch_bwd<T, 4>(q, stream); break;
+    case 8: e = launch_bwd<T, 8>(q, stream); break;
+    default: e = launch_bwd<T, 16>(q, stream); break;
+    }
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+template cudaError_t launch_layer_norm<float>(const NormProblem &, cudaStream_t);
+template cudaError_t launch_layer_norm<__nv_bfloat16>(const NormProblem &, cudaStream_t);
+template cudaError_t launch_layer_norm_backward<float>(const NormBackwardProblem &, cudaStream_t);
+template cudaError_t launch_layer_norm_backward<__nv_bfloat16>(const NormBackwardProblem &, cudaStream_t);
+
+}  // namespace bimamba

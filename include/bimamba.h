@@ -425,6 +425,52 @@ int bimamba_out_proj(int tokens, int d_inner, int d_model, const void *y,
                      const void *w_out, void *out, bimamba_stream_t stream);
 
 /*
+ * The residual add and layer norm in front of a mixer's input projection
+ * ("DiffuMamba" blog post, network-architecture listing: mixer blocks with a
+ * LayerNorm), and its backward pass.  Per row of `cols` elements:
+ *   h = x + residual (h = x without one), in fp32
+ *   mean = mean(h),  rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *   y = (h - mean) rstd gamma + beta
+ *   x         : (rows, cols) dtype
+ *   residual  : (rows, cols) dtype or NULL;  sum_out : (rows, cols) dtype, h
+ *               rounded to dtype -- required with a residual, NULL without
+ *   gamma     : (cols) fp32;  beta : (cols) fp32 or NULL (zero)
+ *   y         : (rows, cols) dtype;  mean, rstd : (rows) fp32
+ * The statistics and y come from the unrounded h; sum_out is what the
+ * residual stream carries on, and what the backward pass takes as h.
+ * eps >= 0.  Outputs must not overlap inputs or each other.
+ *
+ * bimamba_layer_norm_backward: gradients of sum(dy * y) [+ sum(dsum * h)].
+ * With z = (h - mean) rstd and a = dy gamma:
+ *   dx     = rstd (a - mean(a) - z mean(a z)) + dsum   (also d(residual))
+ *   dgamma = sum over rows of dy z,   dbeta = sum over rows of dy
+ *   dy, h  : (rows, cols) dtype (h: x, or sum_out where there was a residual)
+ *   mean, rstd : (rows) fp32, from the forward call
+ *   dsum   : (rows, cols) dtype or NULL -- the gradient that reaches h past
+ *            the norm (through the residual stream)
+ *   dx     : (rows, cols) dtype;  dgamma : (cols) fp32
+ *   dbeta  : (cols) fp32 or NULL (not computed)
+ *   workspace : bimamba_layer_norm_backward_workspace_bytes(rows, cols) bytes,
+ *            16-byte aligned, no clearing needed; calls that share one must
+ *            not run concurrently
+ * The same call gives the same bits every time (no atomics).  rows == 0 is a
+ * valid call (dgamma and dbeta are zeroed).  Both: cols a multiple of 8 up to
+ * 8192 (else BIMAMBA_ERR_UNSUPPORTED), pointers 16-byte aligned.
+ */
+int bimamba_layer_norm(long long rows, int cols, const void *x, const void *residual,
+                       const float *gamma, const float *beta, float eps, void *y,
+                       void *sum_out, float *mean, float *rstd, int dtype,
+                       bimamba_stream_t stream);
+
+size_t bimamba_layer_norm_backward_workspace_bytes(long long rows, int cols);
+
+int bimamba_layer_norm_backward(long long rows, int cols, const void *dy, const void *h,
+                                const float *gamma, const float *mean, const float *rstd,
+                                const void *dsum, void *dx, float *dgamma, float *dbeta,
+                                int dtype, void *workspace, size_t workspace_bytes,
+                                bimamba_stream_t stream);
+
+/*
  * Cached block decode without a caller workspace.  The paper has no
  * counterpart to this entry point; it exists for callers that cannot
  * allocate device memory: a serving process whose memory pool already holds
