@@ -47,6 +47,10 @@ EXPORTED = (
     "bimamba_ssd_fwd_rev_backward",
     "bimamba_in_proj",
     "bimamba_out_proj",
+    "bimamba_prompt_workspace_bytes",
+    "bimamba_prompt_scan",
+    "bimamba_token_step_workspace_bytes",
+    "bimamba_token_step",
     "bimamba_layer_norm",
     "bimamba_layer_norm_backward_workspace_bytes",
     "bimamba_layer_norm_backward",
@@ -111,6 +115,14 @@ def _load() -> ctypes.CDLL:
     lib.bimamba_in_proj.argtypes = [i, i, i, i, i, vp, vp, vp, vp, vp, vp]
     lib.bimamba_out_proj.restype = i
     lib.bimamba_out_proj.argtypes = [i, i, i, vp, vp, vp, vp]
+    lib.bimamba_prompt_workspace_bytes.restype = sz
+    lib.bimamba_prompt_workspace_bytes.argtypes = [dp]
+    lib.bimamba_prompt_scan.restype = i
+    lib.bimamba_prompt_scan.argtypes = [dp] + [vp] * 9 + [i] + [vp] * 4 + [sz, vp]
+    lib.bimamba_token_step_workspace_bytes.restype = sz
+    lib.bimamba_token_step_workspace_bytes.argtypes = [dp]
+    lib.bimamba_token_step.restype = i
+    lib.bimamba_token_step.argtypes = [dp] + [vp] * 8 + [i] + [vp] * 3 + [sz, vp]
     ll, f = ctypes.c_longlong, ctypes.c_float
     lib.bimamba_layer_norm.restype = i
     lib.bimamba_layer_norm.argtypes = [ll, i, vp, vp, vp, vp, f, vp, vp, vp, vp, i, vp]
@@ -419,6 +431,80 @@ class _Args:
         if s is None:
             return torch.cuda.current_stream(index).cuda_stream
         return s if isinstance(s, int) else s.cuda_stream
+
+
+def _causal_args(a, xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state):
+    """The inputs that the prompt scan and the token step share."""
+    rows, f32, td = xbc.shape[0], torch.float32, xbc.dtype
+    ch = heads * headdim + 2 * d_state
+    return (a.ptr("xbc", xbc, td, (rows, ch)), a.ptr("dt", dt, td, (rows, heads)),
+            a.ptr("A", A, f32, (heads,)), a.ptr("D", D, f32, (heads,)),
+            a.ptr("conv_w", conv_w, f32, (ch, 4)), a.opt("conv_b", conv_b, f32, (ch,)))
+
+
+def _pool_args(a, state_pool, tail_pool, dtype, heads, headdim, d_state):
+    pool = state_pool.shape[0]
+    return (a.ptr("state_pool", state_pool, torch.float32, (pool, heads, headdim, d_state)),
+            a.ptr("tail_pool", tail_pool, dtype, (pool, 4, heads * headdim + 2 * d_state)), pool)
+
+
+def bimamba_prompt_workspace_bytes(dims: Dims) -> int:
+    return int(_lib.bimamba_prompt_workspace_bytes(ctypes.byref(dims)))
+
+
+def new_prompt_workspace(xbc, *, batch, heads, headdim, d_state) -> torch.Tensor:
+    """Zero-filled workspace for bimamba_prompt_scan on packed rows like
+    xbc's, for up to `batch` prompts."""
+    n = bimamba_prompt_workspace_bytes(make_dims(batch, xbc.shape[0], heads, headdim, d_state,
+                                                 _dtype_code(xbc)))
+    return torch.zeros(max(256, n), dtype=torch.uint8, device=xbc.device)
+
+
+def bimamba_prompt_scan(xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, tail_pool, slots,
+                        resume, y, workspace, *, heads, headdim, d_state, stream=None):
+    """Causal conv + scan of packed prompts (prompt s: rows cu_seqlens[s] ..
+    cu_seqlens[s+1]-1 of xbc (rows, ch) and dt (rows, H)) into y (rows, H*P);
+    pool entry slots[s] gets the prompt's state and last raw tokens, and is
+    what it continues from where resume[s] != 0 (resume None: nowhere).
+    cu_seqlens, slots and resume are int32 device tensors."""
+    a = _Args("bimamba_prompt_scan", xbc, stream)
+    td, n, i32 = xbc.dtype, slots.shape[0], torch.int32
+    dims = make_dims(n, xbc.shape[0], heads, headdim, d_state, _dtype_code(xbc))
+    inputs = _causal_args(a, xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state)
+    pool = _pool_args(a, state_pool, tail_pool, td, heads, headdim, d_state)
+    ws, ws_bytes = a.workspace(workspace)
+    a.call(_lib.bimamba_prompt_scan, ctypes.byref(dims), *inputs,
+           a.ptr("cu_seqlens", cu_seqlens, i32, (n + 1,)), *pool, a.ptr("slots", slots, i32, (n,)),
+           a.opt("resume", resume, i32, (n,)), a.ptr("y", y, td, (xbc.shape[0], heads * headdim)), ws,
+           ws_bytes)
+    return y
+
+
+def bimamba_token_step_workspace_bytes(dims: Dims) -> int:
+    return int(_lib.bimamba_token_step_workspace_bytes(ctypes.byref(dims)))
+
+
+def new_step_workspace(rows, *, heads, headdim, d_state, dtype, device=None) -> torch.Tensor:
+    """Zero-filled workspace for bimamba_token_step on up to `rows` rows."""
+    n = bimamba_token_step_workspace_bytes(make_dims(rows, 1, heads, headdim, d_state, dtype))
+    return torch.zeros(max(256, n), dtype=torch.uint8, device=device or "cuda")
+
+
+def bimamba_token_step(xbc, dt, A, D, conv_w, conv_b, state_pool, tail_pool, slots, y, workspace, *,
+                       heads, headdim, d_state, stream=None):
+    """One new token of each of a batch of cached streams: row s of xbc
+    (rows, ch) and dt (rows, H) continues from pool entry slots[s], which is
+    updated in place, into row s of y (rows, H*P)."""
+    a = _Args("bimamba_token_step", xbc, stream)
+    td, rows = xbc.dtype, xbc.shape[0]
+    dims = make_dims(rows, 1, heads, headdim, d_state, _dtype_code(xbc))
+    inputs = _causal_args(a, xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state)
+    pool = _pool_args(a, state_pool, tail_pool, td, heads, headdim, d_state)
+    ws, ws_bytes = a.workspace(workspace)
+    a.call(_lib.bimamba_token_step, ctypes.byref(dims), *inputs, *pool,
+           a.ptr("slots", slots, torch.int32, (rows,)), a.ptr("y", y, td, (rows, heads * headdim)), ws,
+           ws_bytes)
+    return y
 
 
 def bimamba_layer_norm(x, gamma, beta, y, mean, rstd, *, residual=None, sum_out=None, eps=1e-5,

@@ -458,6 +458,102 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block, cons
                                                d->batch, d->len, ch, device_status_word(), s));
 }
 
+// What bimamba_prompt_scan and bimamba_token_step check alike.
+static int check_causal(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
+                        const float *D, const float *conv_w, const float *conv_b,
+                        const int *cu_seqlens, const float *state_pool, const void *tail_pool,
+                        int pool_size, const int *slots, const int *resume, const void *y,
+                        const void *workspace, size_t workspace_bytes, size_t need)
+{
+    if (pool_size < 1 || !A || !D || !conv_w || !state_pool || !tail_pool || !slots)
+        return BIMAMBA_ERR_INVALID;
+    if (d->len > 0 && (!xbc || !dt || !y)) return BIMAMBA_ERR_INVALID;
+    const void *ptrs[] = {xbc, dt, A, D, conv_w, conv_b, state_pool, tail_pool, y};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return BIMAMBA_ERR_INVALID;
+    const void *ints[] = {cu_seqlens, slots, resume};
+    for (const void *p : ints)
+        if (p && (reinterpret_cast<uintptr_t>(p) & 3u)) return BIMAMBA_ERR_INVALID;
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return BIMAMBA_ERR_WORKSPACE;
+    const size_t esz = d->dtype == BIMAMBA_F32 ? 4 : 2, nb = (size_t)d->batch;
+    const size_t inner = (size_t)d->heads * d->headdim, ch = inner + 2 * (size_t)d->d_state;
+    const size_t nx = ch * esz, rows = cu_seqlens ? (size_t)d->len : nb;
+    const Range r[] = {{y, rows * inner * esz},
+                       {state_pool, (size_t)pool_size * inner * d->d_state * 4},
+                       {tail_pool, (size_t)pool_size * 4 * nx},
+                       {workspace, need},
+                       {xbc, rows * nx},
+                       {dt, rows * d->heads * esz},
+                       {A, (size_t)d->heads * 4},
+                       {D, (size_t)d->heads * 4},
+                       {conv_w, ch * 16},
+                       {conv_b, ch * 4},
+                       {cu_seqlens, (nb + 1) * 4},
+                       {slots, nb * 4},
+                       {resume, nb * 4}};
+    return any_output_overlaps(r, 4, 13) ? BIMAMBA_ERR_INVALID : BIMAMBA_OK;
+}
+
+size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d)
+{
+    if (check_dims(d) != BIMAMBA_OK) return 0;
+    return prompt_ticket_bytes(*d);
+}
+
+int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
+                        const float *D, const float *conv_w, const float *conv_b,
+                        const int *cu_seqlens, float *state_pool, void *tail_pool, int pool_size,
+                        const int *slots, const int *resume, void *y, void *workspace,
+                        size_t workspace_bytes, bimamba_stream_t stream)
+{
+    int st = check_dims(d);
+    if (st != BIMAMBA_OK) return st;
+    if (d->batch == 0) return BIMAMBA_OK;
+    if (!cu_seqlens) return BIMAMBA_ERR_INVALID;
+    st = check_causal(d, xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, tail_pool, pool_size,
+                      slots, resume, y, workspace, workspace_bytes, bimamba_prompt_workspace_bytes(d));
+    if (st != BIMAMBA_OK) return st;
+    PromptProblem q{};
+    q.dims = *d;
+    q.xbc = xbc; q.dt = dt; q.A = A; q.D = D; q.conv_w = conv_w; q.conv_b = conv_b;
+    q.cu_seqlens = cu_seqlens;
+    q.state = state_pool; q.tail = tail_pool; q.pool = pool_size; q.slots = slots; q.resume = resume;
+    q.y = y;
+    q.tickets = static_cast<int *>(workspace);
+    q.workspace = static_cast<char *>(workspace) + prompt_ticket_bytes(*d);
+    q.status = device_status_word();
+    return cuda_status(launch_prompt(q, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t bimamba_token_step_workspace_bytes(const bimamba_dims *d)
+{
+    if (check_dims(d) != BIMAMBA_OK) return 0;
+    return prompt_ticket_bytes(*d);
+}
+
+int bimamba_token_step(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
+                       const float *D, const float *conv_w, const float *conv_b, float *state_pool,
+                       void *tail_pool, int pool_size, const int *slots, void *y, void *workspace,
+                       size_t workspace_bytes, bimamba_stream_t stream)
+{
+    int st = check_dims(d);
+    if (st != BIMAMBA_OK) return st;
+    if (d->len != 1) return BIMAMBA_ERR_INVALID;
+    if (d->batch == 0) return BIMAMBA_OK;
+    st = check_causal(d, xbc, dt, A, D, conv_w, conv_b, nullptr, state_pool, tail_pool, pool_size,
+                      slots, nullptr, y, workspace, workspace_bytes, prompt_ticket_bytes(*d));
+    if (st != BIMAMBA_OK) return st;
+    StepProblem q{};
+    q.rows = d->batch; q.H = d->heads; q.P = d->headdim; q.N = d->d_state; q.pool = pool_size;
+    q.xbc = xbc; q.dt = dt; q.A = A; q.D = D; q.conv_w = conv_w; q.conv_b = conv_b;
+    q.state = state_pool; q.tail = tail_pool; q.slots = slots; q.y = y;
+    q.tickets = static_cast<int *>(workspace);
+    q.status = device_status_word();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(d->dtype == BIMAMBA_F32 ? launch_token_step<float>(q, s)
+                                               : launch_token_step<__nv_bfloat16>(q, s));
+}
+
 int bimamba_in_proj(int tokens, int d_model, int heads, int headdim, int d_state, const void *u,
                     const void *w_in, const float *dt_bias, void *xbc, void *dt,
                     bimamba_stream_t stream)

@@ -23,4 +23,15 @@ cudaError_t launch_bimamba(const Problem &p, cudaStream_t stream)
     return launch_scan_seq<__nv_bfloat16>(p, stream);
 }
 
+size_t prompt_ticket_bytes(const bimamba_dims &d)
+{
+    return ((size_t)d.batch * sizeof(int) + 255) & ~(size_t)255;
+}
+
+cudaError_t launch_prompt(const PromptProblem &q, cudaStream_t stream)
+{
+    if (q.dims.dtype == BIMAMBA_F32) return launch_prompt_seq<float>(q, stream);
+    return launch_prompt_seq<__nv_bfloat16>(q, stream);
+}
+
 }  // namespace bimamba

@@ -127,6 +127,42 @@ bool backward_tc_supported(const bimamba_dims &d);
 size_t backward_tc_state_bytes(const bimamba_dims &d);
 cudaError_t launch_backward_tc(const BackwardTcProblem &q, cudaStream_t stream);
 
+// the causal mixer core over packed prompts, from and into a state pool
+struct PromptProblem {
+    bimamba_dims dims;            // batch = prompts, len = packed rows
+    const void *xbc, *dt;
+    const float *A, *D, *conv_w, *conv_b;
+    const int *cu_seqlens;        // (batch + 1)
+    float *state;                 // (pool, H, P, N)
+    void *tail;                   // (pool, 4, ch)
+    int pool;
+    const int *slots, *resume;    // (batch); resume may be null
+    void *y;
+    int *tickets;                 // (batch) zeros, returned to zero
+    void *workspace;
+    int *status;
+};
+// leading bytes of both operators' workspaces: the tickets
+size_t prompt_ticket_bytes(const bimamba_dims &d);
+cudaError_t launch_prompt(const PromptProblem &q, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_prompt_seq(const PromptProblem &q, cudaStream_t stream);
+
+// one token per cached stream
+struct StepProblem {
+    int rows, H, P, N, pool;
+    const void *xbc, *dt;
+    const float *A, *D, *conv_w, *conv_b;
+    float *state;
+    void *tail;
+    const int *slots;
+    void *y;
+    int *tickets;                 // (rows) zeros, returned to zero
+    int *status;
+};
+template <typename T>
+cudaError_t launch_token_step(const StepProblem &q, cudaStream_t stream);
+
 // (residual add and) layer norm, and its backward pass
 struct NormProblem {
     long long rows;

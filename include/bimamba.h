@@ -355,6 +355,68 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
                               bimamba_stream_t stream);
 
 /*
+ * Causal mixer core over a batch of prompts, filling the pool that
+ * bimamba_block_decode_pool and bimamba_token_step decode from: conv + SiLU
+ * and the forward recurrence written at the top of this file, without the
+ * reverse stream.  "Fixed state, long reach: constant-size caches in
+ * large-scale block diffusion", abstract and section 1: a finished prefix is
+ * cached as the forward SSM state and its last raw tokens.  The prompts are
+ * packed one after another and may have any lengths, zero among them.
+ *   d          : batch = prompts, len = rows of xbc (packed tokens)
+ *   xbc        : (len, ch) raw xBC, dtype;  dt : (len, H) dtype, positive
+ *   A, D, conv_w (required), conv_b (nullable) : as above
+ *   cu_seqlens : (batch + 1) int32, device -- prompt s is the rows
+ *                cu_seqlens[s] .. cu_seqlens[s + 1] - 1; rows outside every
+ *                prompt are not read and their y is left as it was
+ *   state_pool : (pool_size, H, P, N) fp32;  tail_pool : (pool_size, 4, ch)
+ *                dtype -- prompt s's entry slots[s] gets its state after the
+ *                last token and its last 4 raw tokens, in place
+ *   slots      : (batch) int32, device
+ *   resume     : (batch) int32, device, or NULL (no prompt resumes) --
+ *                resume[s] != 0 continues from the entry's state and tail,
+ *                else the prompt starts from zeros.  An empty prompt that
+ *                resumes leaves its entry as it is, one that does not zeroes it.
+ *   y          : (len, H*P) dtype
+ *   workspace  : bimamba_prompt_workspace_bytes(d) bytes, 256-byte aligned,
+ *                zero-filled before its first use; a call leaves it fit for
+ *                the next call with any dims it is large enough for.  Calls
+ *                that share one (two graphs, too) must not run concurrently.
+ * What only the device knows is checked there: a prompt whose slot is
+ * outside [0, pool_size) or is another prompt's too, or whose rows are not a
+ * range inside [0, len), is skipped (y and the pool untouched) and makes
+ * bimamba_get_error report BIMAMBA_ERR_INVALID.  A negative slot marks a
+ * padding entry of the batch: skipped without an error.
+ * y must not overlap an input or the pool.
+ */
+size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d);
+
+int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
+                        const float *D, const float *conv_w, const float *conv_b,
+                        const int *cu_seqlens, float *state_pool, void *tail_pool,
+                        int pool_size, const int *slots, const int *resume, void *y,
+                        void *workspace, size_t workspace_bytes, bimamba_stream_t stream);
+
+/*
+ * One new token of each of a batch of cached streams (causal, same sources
+ * as bimamba_prompt_scan): row s continues from its pool entry and updates
+ * the entry's state and tail in place.
+ *   d    : batch = rows, len = 1 (else BIMAMBA_ERR_INVALID)
+ *   xbc  : (batch, ch) raw xBC, dtype;  dt : (batch, H) dtype, positive
+ *   y    : (batch, H*P) dtype
+ *   the others as in bimamba_prompt_scan; workspace:
+ *   bimamba_token_step_workspace_bytes(d) bytes, zero-filled before its
+ *   first use (same rules).  Row s's result equals a prompt of one token
+ *   that resumes.  Bad, repeated and negative slots as there.
+ */
+size_t bimamba_token_step_workspace_bytes(const bimamba_dims *d);
+
+int bimamba_token_step(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
+                       const float *D, const float *conv_w, const float *conv_b,
+                       float *state_pool, void *tail_pool, int pool_size, const int *slots,
+                       void *y, void *workspace, size_t workspace_bytes,
+                       bimamba_stream_t stream);
+
+/*
  * Backward pass of the bidirectional mixer core (training): the gradients of
  * L = sum(dy * y), y = bimamba_ssd_fwd_rev(xbc, dt, A, D, conv_w, conv_b,
  * init_state), with respect to every input.  "DiffuMamba: High-Throughput
