@@ -497,7 +497,7 @@ static int check_causal(const bimamba_dims *d, const void *xbc, const void *dt, 
 size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d)
 {
     if (check_dims(d) != BIMAMBA_OK) return 0;
-    return prompt_ticket_bytes(*d);
+    return prompt_ticket_bytes(*d) + (prompt_tc_supported(*d) ? prompt_tc_ws_bytes(*d) : 0);
 }
 
 int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,

@@ -30,6 +30,9 @@ size_t prompt_ticket_bytes(const bimamba_dims &d)
 
 cudaError_t launch_prompt(const PromptProblem &q, cudaStream_t stream)
 {
+    // as for the bidirectional scan: the tensor cores for bf16 at the model's
+    // head shape, fp32 and other head shapes on the CUDA cores
+    if (prompt_tc_supported(q.dims)) return launch_prompt_tc(q, stream);
     if (q.dims.dtype == BIMAMBA_F32) return launch_prompt_seq<float>(q, stream);
     return launch_prompt_seq<__nv_bfloat16>(q, stream);
 }

@@ -147,6 +147,9 @@ size_t prompt_ticket_bytes(const bimamba_dims &d);
 cudaError_t launch_prompt(const PromptProblem &q, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_prompt_seq(const PromptProblem &q, cudaStream_t stream);
+bool prompt_tc_supported(const bimamba_dims &d);   // bf16, headdim 64, d_state 128, even heads
+size_t prompt_tc_ws_bytes(const bimamba_dims &d);
+cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream);
 
 // one token per cached stream
 struct StepProblem {

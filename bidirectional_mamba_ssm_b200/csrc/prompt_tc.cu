@@ -1,0 +1,1279 @@
+// prompt_tc.cu -- the causal mixer core over packed ragged prompts on the
+// sm_100a tensor cores (bf16 activations, headdim 64, d_state 128).
+//
+// Operation (Mamba-2 recurrence, d_conv = 4; the cache entry of "Fixed state,
+// long reach: constant-size caches in large-scale block diffusion"), for each
+// prompt from its pool entry's state and tail (or zeros), per head:
+//     u_t = SiLU(bias + sum_j w_j raw_{t-3+j})        (x, B and C channels)
+//     h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t^T,   y_t = h_t C_t + D x_t
+//
+// Chunked form (chunks of 128 tokens from the prompt's own start; c_t =
+// inclusive prefix sum of dt A in the chunk, S = state entering it):
+//     G       = C B^T
+//     M[t,s]  = G[t,s] exp(c_t - c_s) dt_s  (s < t),  G[t,t] dt_t + D  (s = t)
+//     Y       = exp(c_t) (C S^T) + M X
+//     S      <- exp(c_last) S + (w o X)^T B,    w_s = exp(c_last - c_s) dt_s
+//
+// Precision.  y is stored in bf16, so its operands (C, B, X, M, a copy of S)
+// are bf16.  The state is kept and handed on in fp32 over any number of
+// tokens, so its update is not: w o X and B enter as two bf16 halves each
+// (value = hi + lo to 2^-17) and three products, hi hi + lo hi + hi lo; the
+// conv, SiLU and decays before them are fp32, exp(c_last - c_s) comes from
+// suffix sums (no cancellation where it matters), and a slow decay is applied
+// as S + S expm1(c_last), whose error does not add up over thousands of
+// chunks.
+//
+// Kernels of one call:
+//   1. plan + conv of B and C: per 128-token chunk the operand rows
+//      [B hi | B lo | C] (zeros behind the prompt's end, so that a neighbour
+//      never enters a product), and, by one CTA, the table of walks.
+//   2. only where a prompt may be long against the GPU's share of the work
+//      (segment_chunks): prompts above that are cut into equal segments; a
+//      state-only walk of each segment but the last, then
+//   3. the states that enter the segments, chained over them.
+//   4. one walk per (segment, head pair): all products on tcgen05, the state
+//      in tensor memory.
+//
+// Bounds of the walk, per chunk and head pair: 56 MMAs of 65 cycles (8 G, 8
+// C S^T, 16 M X, 24 state) = 3.6K cycles, and about 14K warp instructions
+// (conv and SiLU, operand splitting, M, state and output scaling) = 3.5K
+// cycles of the four schedulers; HBM 66 KB = 1.5K cycles at the SM's share.
+#include "common.cuh"
+#include "dispatch.h"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+namespace bimamba {
+
+namespace {
+
+constexpr int kQ = 128;            // tokens per chunk
+constexpr int kP = 64, kN = 128;   // headdim and d_state of this path
+constexpr int kPP = 2 * kP;        // x channels of a head pair
+constexpr int kAct = 3 * kN;       // operand row: B hi | B lo | C
+constexpr int kRawRows = kQ + 3;   // raw x rows of a chunk with the conv halo
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr long long kWaitCycles = 4000000000LL;   // ~2 s: bound of every wait
+
+// One walk: `chunks` chunks of prompt `seq` from chunk `chunk`, whose operand
+// rows start at chunk `act` of the operand array.
+struct Walk {
+    int seq, chunk, chunks, act;
+    int slot;          // entering state's slot (prompts in segments), or -1
+    int last;          // the prompt's last segment
+    int pad0, pad1;
+};
+
+struct PlanHeader {
+    int inner, total;  // walks that are not their prompt's last; all walks
+    int pad0, pad1;
+};
+
+struct PromptParams {
+    const __nv_bfloat16 *xbc, *dt;
+    const float *A, *D, *conv_w, *conv_b;
+    const int *cu, *slots, *resume;
+    float *state;            // pool
+    __nv_bfloat16 *tail;     // pool
+    __nv_bfloat16 *y, *act;
+    PlanHeader *head;
+    Walk *walks;
+    int2 *segs;              // per prompt: first slot, segments (1: whole)
+    float *seg_state;        // [slot][H][kP][kN]
+    float *seg_dec;          // [slot][H], log2 of the segment's decay before it
+    int *status;
+    int batch, len, H, ch, pool;
+    int max_chunks;          // chunks of the operand array
+    int seg_chunks;          // prompts above this are cut
+};
+
+// Prompt s as the plan sees it: its chunks, or none where its slot or range
+// is not usable (`bad`: to be reported).
+struct Prompt {
+    int begin, len, chunks;
+    bool ok, bad;
+};
+__device__ __forceinline__ Prompt read_prompt(const PromptParams &p, int s)
+{
+    Prompt r{0, 0, 0, false, false};
+    if (s >= p.batch) return r;
+    const int slot = p.slots[s];
+    r.begin = p.cu[s];
+    const int end = p.cu[s + 1];
+    r.ok = slot >= 0 && slot < p.pool && r.begin >= 0 && end >= r.begin && end <= p.len;
+    r.bad = !r.ok && slot >= 0;
+    if (r.ok) {
+        r.len = end - r.begin;
+        r.chunks = (r.len + kQ - 1) / kQ;
+    }
+    return r;
+}
+
+constexpr int kPrepThreads = 256;
+
+// Exclusive prefix sum over the CTA's threads, and the total.
+__device__ __forceinline__ int block_scan(int v, int *total)
+{
+    __shared__ int part[kPrepThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += t;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = run;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+        if (w < warp) before += part[w];
+        all += part[w];
+    }
+    *total = all;
+    return before + run - v;
+}
+
+__device__ __forceinline__ float silu_approx(float a)
+{
+    // a sigmoid(a), off by a few 2^-23 (the hardware tanh's 2^-11 would do for
+    // y but not for the state)
+    return __fdividef(a, 1.0f + tc::exp2_approx(-kLog2e * a));
+}
+
+// hi = the bf16 nearest to v, lo = the bf16 nearest to v - hi, for two values.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    hi = tc::pack_bf16x2(a, b);
+    const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+    lo = tc::pack_bf16x2(ra, rb);
+}
+
+}  // namespace
+
+// Plan (the last CTA) and B/C operand rows (one CTA per chunk of the operand
+// array).  A thread convolves 8 channels of 16 tokens.
+__global__ void __launch_bounds__(kPrepThreads)
+prompt_prep_kernel(const PromptParams p)
+{
+    const int tid = threadIdx.x;
+    const int me = blockIdx.x;
+    if (me == p.max_chunks) {
+        // ---- the table of walks.  First the walks that are not a prompt's
+        // last segment (the state-only walks take exactly these), then the
+        // last ones, longer before shorter in four classes, so that the long
+        // walks start first.
+        int inner = 0, chunks = 0;
+        int cls[4] = {0, 0, 0, 0};
+        auto shape = [&](const Prompt &r, int &nseg, int &seg) {
+            nseg = r.chunks > p.seg_chunks ? (r.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
+            seg = nseg > 1 ? (r.chunks + nseg - 1) / nseg : r.chunks;
+            if (nseg > 1) nseg = (r.chunks + seg - 1) / seg;
+        };
+        auto class_of = [&](int n) { return min(3, 4 * n / (p.seg_chunks + 1)); };
+        for (int s0 = 0; s0 < p.batch; s0 += kPrepThreads) {
+            Prompt r = read_prompt(p, s0 + tid);
+            if (r.bad) record_error(p.status, kStatusBadSlot);
+            int all, nseg, seg;
+            const int at = chunks + block_scan(r.chunks, &all);
+            chunks += all;
+            if (r.ok && at + r.chunks > p.max_chunks) {   // ranges that overlap: more rows than there are
+                r.ok = false;
+                record_error(p.status, kStatusBadSlot);
+            }
+            shape(r, nseg, seg);
+            block_scan(r.ok ? nseg - 1 : 0, &all);
+            inner += all;
+            const int c = class_of(r.chunks - (nseg - 1) * seg);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                block_scan(r.ok && c == q, &all);
+                cls[q] += all;
+            }
+        }
+        int next[4];   // first walk of each class
+        next[3] = inner;
+        next[2] = next[3] + cls[3];
+        next[1] = next[2] + cls[2];
+        next[0] = next[1] + cls[1];
+        if (tid == 0) *p.head = PlanHeader{inner, next[0] + cls[0], 0, 0};
+        int inner_at = 0, slot_at = 0;
+        chunks = 0;
+        for (int s0 = 0; s0 < p.batch; s0 += kPrepThreads) {
+            const int s = s0 + tid;
+            Prompt r = read_prompt(p, s);
+            int all, nseg, seg;
+            const int at = chunks + block_scan(r.chunks, &all);
+            chunks += all;
+            if (at + r.chunks > p.max_chunks) r.ok = false;
+            shape(r, nseg, seg);
+            const bool cut = r.ok && nseg > 1;
+            const int wi = inner_at + block_scan(cut ? nseg - 1 : 0, &all);
+            inner_at += all;
+            const int slot = slot_at + block_scan(cut ? nseg : 0, &all);
+            slot_at += all;
+            const int tail_chunks = r.chunks - (nseg - 1) * seg;
+            const int c = class_of(tail_chunks);
+            int wl = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int at_q = next[q] + block_scan(r.ok && c == q, &all);
+                next[q] += all;
+                if (c == q) wl = at_q;
+            }
+            if (s < p.batch) p.segs[s] = make_int2(slot, cut ? nseg : 1);
+            if (!r.ok) continue;
+            for (int i = 0; i < nseg - 1; ++i)
+                p.walks[wi + i] = Walk{s, i * seg, seg, at + i * seg, slot + i, 0, 0, 0};
+            const int first = (nseg - 1) * seg;
+            p.walks[wl] = Walk{s, first, tail_chunks, at + first, cut ? slot + nseg - 1 : -1, 1, 0, 0};
+        }
+        return;
+    }
+
+    // ---- which prompt's chunk is chunk `me` of the operand array
+    __shared__ int4 found;   // prompt, chunk in it, begin, len
+    if (tid == 0) found = make_int4(-1, 0, 0, 0);
+    int chunks = 0;
+    for (int s0 = 0; s0 < p.batch && chunks <= me; s0 += kPrepThreads) {
+        const Prompt r = read_prompt(p, s0 + tid);
+        int all;
+        const int at = chunks + block_scan(r.chunks, &all);
+        chunks += all;
+        if (r.ok && at <= me && me < at + r.chunks && at + r.chunks <= p.max_chunks)
+            found = make_int4(s0 + tid, me - at, r.begin, r.len);
+    }
+    __syncthreads();
+    const int4 f = found;
+    if (f.x < 0) return;
+    const int g = tid & 31, sub = tid >> 5;
+    const int n0 = 8 * g;                      // channels n0 .. n0 + 7 of [B | C]
+    const int c = p.H * kP + n0;
+    const int t0 = f.y * kQ + sub * 16;        // first token of this thread in the prompt
+    const __nv_bfloat16 *raw = p.xbc + (size_t)f.z * p.ch + c;
+    const bool resume = p.resume && p.resume[f.x] != 0;
+    const __nv_bfloat16 *tail = p.tail + (size_t)p.slots[f.x] * 4 * p.ch + c;
+    float w[8][4], bias[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 t = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(c + q) * 4);
+        w[q][0] = t.x; w[q][1] = t.y; w[q][2] = t.z; w[q][3] = t.w;
+        bias[q] = p.conv_b ? p.conv_b[c + q] : 0.0f;
+    }
+    __nv_bfloat16 *out = p.act + ((size_t)me * kQ + sub * 16) * kAct;
+    auto at = [&](int t) -> uint4 {
+        if (t >= f.w) return make_uint4(0u, 0u, 0u, 0u);
+        if (t >= 0) return *reinterpret_cast<const uint4 *>(raw + (size_t)t * p.ch);
+        return resume ? *reinterpret_cast<const uint4 *>(tail + (size_t)(4 + t) * p.ch) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 rows[11];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) rows[i] = at(t0 - 3 + i);
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rows[3 + i] = at(t0 + 8 * half + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + 8 * half + i;
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = bias[q];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&rows[i + j]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 v = __bfloat1622float2(h[q]);
+                    o[2 * q] = fmaf(w[2 * q][j], v.x, o[2 * q]);
+                    o[2 * q + 1] = fmaf(w[2 * q + 1][j], v.y, o[2 * q + 1]);
+                }
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool in = t < f.w;
+                split2(in ? silu_approx(o[2 * q]) : 0.0f, in ? silu_approx(o[2 * q + 1]) : 0.0f, hi[q], lo[q]);
+            }
+            __nv_bfloat16 *row = out + (size_t)(8 * half + i) * kAct;
+            if (n0 < kN) {
+                *reinterpret_cast<uint4 *>(row + n0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(row + kN + n0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+                *reinterpret_cast<uint4 *>(row + kN + n0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) rows[i] = rows[8 + i];
+    }
+}
+
+// The states entering each segment of a cut prompt, over its slots in order:
+// slot i holds the end state from zero of segment i - 1 (and its decay) and
+// gets E_i, E_0 = the prompt's initial state, E_i = 2^dec E_{i-1} + S_{i-1}.
+__global__ void __launch_bounds__(256)
+prompt_chain_kernel(const PromptParams p)
+{
+    const int s = blockIdx.y;
+    const int2 seg = p.segs[s];
+    if (seg.y <= 1) return;
+    const int e = blockIdx.x * 256 + threadIdx.x;   // float4 of the state
+    const int per = p.H * kP * kN / 4;
+    if (e >= per) return;
+    const int h = e / (kP * kN / 4);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.resume && p.resume[s] != 0)
+        v = reinterpret_cast<const float4 *>(p.state)[(size_t)p.slots[s] * per + e];
+    float4 *st = reinterpret_cast<float4 *>(p.seg_state) + (size_t)seg.x * per + e;
+    *st = v;
+    for (int i = 1; i < seg.y; ++i) {
+        st += per;
+        const float a = exp2f(p.seg_dec[(size_t)(seg.x + i) * p.H + h]);
+        const float4 q = *st;
+        v.x = fmaf(a, v.x, q.x);
+        v.y = fmaf(a, v.y, q.y);
+        v.z = fmaf(a, v.z, q.z);
+        v.w = fmaf(a, v.w, q.w);
+        *st = v;
+    }
+}
+
+namespace {
+
+// ---- the walk kernel's shared memory (bytes from a 1024-aligned base)
+constexpr uint32_t kTile = 32768;                   // 128 x 128 bf16: two 64-wide swizzled blocks
+constexpr uint32_t kOffC = 0;                       // C  [t][n]
+constexpr uint32_t kOffBh = kOffC + kTile;          // B hi [s][n]
+constexpr uint32_t kOffBl = kOffBh + kTile;         // B lo [s][n]
+constexpr uint32_t kXbufBytes = 33792;              // raw x [131][128] -> X^T [p'][s] -> output rows
+constexpr uint32_t kOffX0 = kOffBl + kTile;         // even chunks
+constexpr uint32_t kOffX1 = kOffX0 + kXbufBytes;    // odd chunks
+constexpr uint32_t kOffS = kOffX1 + kXbufBytes;     // bf16 copy of the state [p'][n]
+constexpr uint32_t kOffFac = kOffS + kTile;         // per-slot factors, f32 [2 parity][2 head][128] each:
+constexpr uint32_t kFac = 2 * 2 * kQ * 4;
+constexpr uint32_t kOffCum = kOffFac;               //   prefix sums of dt A, log2 units
+constexpr uint32_t kOffDt = kOffCum + kFac;         //   dt
+constexpr uint32_t kOffFB = kOffDt + kFac;          //   exp(c_R - c_s) dt_s, R = end of s's 32-slot block
+constexpr uint32_t kOffF4 = kOffFB + kFac;          //   exp(c_R4 - c_s) dt_s, R4 = s | 3
+constexpr uint32_t kOffWgt = kOffF4 + kFac;         //   w_s
+constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]: see scale_state
+constexpr uint32_t kOffDtBuf = kOffScale + 32;      // [2][128] bf16x2: dt of both heads
+constexpr uint32_t kOffMbar = kOffDtBuf + 2 * kQ * 4;
+constexpr uint32_t kOffTmem = kOffMbar + 160;
+constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
+constexpr uint32_t kRawBytes = kRawRows * kPP * 2;
+static_assert(kOffX0 % 1024 == 0 && kOffX1 % 1024 == 0 && kOffS % 1024 == 0, "tile alignment");
+static_assert(kRawBytes <= kXbufBytes && kSmemBytes <= 227 * 1024, "shared memory");
+
+// ---- tensor memory columns
+constexpr uint32_t kColG = 0;      // G, then in place [M_0 | M_1] per 16 tokens (8 + 8 columns of bf16 pairs)
+constexpr uint32_t kColY = 128;    // Y, 64 columns per head
+constexpr uint32_t kColW = 256;    // (w o X)^T, A operand: 64 columns hi, 64 columns lo
+constexpr uint32_t kColS = 384;    // S [p' = lane][n], fp32
+
+// ---- warps: three groups of 8 and three single ones
+constexpr int kGroup = 256;
+constexpr int kProducerWarp = 24, kHelperWarp = 25, kPublisherWarp = 26;
+constexpr int kThreads = 27 * 32;
+
+__device__ __forceinline__ void grp_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+__device__ __forceinline__ bool grp_and(int id, bool pred)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "bar.red.and.pred q, %1, 256, p;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"((uint32_t)pred) : "memory");
+    return r != 0;
+}
+
+}  // namespace
+
+// One walk of one head pair.  kStateOnly: from a zero state, writing the end
+// state and decay of a segment, no outputs.
+//
+// Warp roles (hand-offs through mbarriers, every wait bounded; [k] = once
+// per chunk):
+//   warps 0..7   M group: M(k) in place over G(k).
+//   warps 8..15  Y group: the state scaled for chunk k with its bf16 copy;
+//                the rows of C S^T scaled by exp(c_t) in place, ready for M X
+//                to be added; the finished rows to the chunk's x buffer.
+//   warps 16..23 X group: conv + SiLU of the chunk's raw rows; X^T in place in
+//                the x buffer, both halves of (w o X)^T to tensor memory.
+//                (lane = channel, so that a thread's tokens are consecutive:
+//                16-byte stores of X^T, and the A operand's layout.)
+//   warp 24      producer: every MMA, the B/C tile loads.
+//   warp 25      helper: dt copies, prefix sums and factors, two chunks ahead.
+//   warp 26      publisher: finished rows to y, then the x load of chunk k+2.
+template <bool kStateOnly>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_bc,
+                   const __grid_constant__ CUtensorMap tm_y, const PromptParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = tc::smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = p.H, ch = p.ch, HP = H / 2;
+    const int hp = blockIdx.x % HP;
+    const int wi = blockIdx.x / HP;
+    if (wi >= (kStateOnly ? p.head->inner : p.head->total)) return;
+    const Walk wk = p.walks[wi];
+    const int slot = p.slots[wk.seq];
+    const int begin = p.cu[wk.seq], len = p.cu[wk.seq + 1] - begin;
+    const bool resume = p.resume && p.resume[wk.seq] != 0;
+    const int nk = wk.chunks;
+    __nv_bfloat16 *tail = p.tail + (size_t)slot * 4 * ch;
+    if constexpr (!kStateOnly) {
+        // an entry that two prompts name belongs to neither
+        bool twice = false;
+        for (int r = tid; r < p.batch; r += kThreads) twice |= r != wk.seq && p.slots[r] == slot;
+        if (__syncthreads_or(twice)) {
+            if (hp == 0 && wk.last && tid == 0) record_error(p.status, kStatusBadSlot);
+            return;
+        }
+    }
+
+    float *cum = reinterpret_cast<float *>(sm + kOffCum);
+    float *dts = reinterpret_cast<float *>(sm + kOffDt);
+    float *fB = reinterpret_cast<float *>(sm + kOffFB);
+    float *f4 = reinterpret_cast<float *>(sm + kOffF4);
+    float *wgt = reinterpret_cast<float *>(sm + kOffWgt);
+    float2 *scl = reinterpret_cast<float2 *>(sm + kOffScale);
+    const uint32_t mb = sbase + kOffMbar;
+    const uint32_t mb_bc = mb;            // [k] B/C tiles landed (state-only: even chunks, odd ones at mb_g)
+    const uint32_t mb_x0 = mb + 8;        // raw x landed in buffer k % 2 (+8)
+    const uint32_t mb_g = mb + 24;        // [k] G done
+    const uint32_t mb_m = mb + 32;        // [k] M ready
+    const uint32_t mb_s = mb + 40;        // [k] state scaled, its copy ready
+    const uint32_t mb_yo = mb + 48;       // [k] C S^T done
+    const uint32_t mb_ys = mb + 56;       // [k] its rows scaled
+    const uint32_t mb_e = mb + 64;        // [k] M X done
+    const uint32_t mb_st = mb + 72;       // [k] rows staged, Y columns free
+    // the rest one for even and one for odd chunks (+8): a wait may come
+    // after the next chunk's phase has completed, never after the next but one
+    const uint32_t mb_w0 = mb + 80;       // X^T and (w o X)^T ready
+    const uint32_t mb_sd0 = mb + 96;      // state product done
+    const uint32_t mb_dt0 = mb + 112;     // factors ready
+    const uint32_t mb_free0 = mb + 128;   // their buffer free
+    auto of = [](uint32_t pair, int k) { return pair + 8 * (k & 1); };
+    auto phase = [](int k) -> uint32_t { return (k >> 1) & 1; };   // of a pair's barrier
+    auto xbuf = [](int k) { return (k & 1) ? kOffX1 : kOffX0; };
+    // chunk k's rows in the prompt
+    auto tokens = [&](int k) { return min(kQ, len - (wk.chunk + k) * kQ); };
+    auto first_row = [&](int k) { return begin + (wk.chunk + k) * kQ; };
+
+    auto issue_x = [&](int k) {
+        const uint32_t bar = mb_x0 + 8 * (k & 1);
+        tc::mbar_expect_tx(bar, kRawBytes);
+        tc::tma_load_3d(sbase + xbuf(k), &tm_x, hp * kPP, first_row(k) - 3, 0, bar);
+    };
+    // B (hi and lo) and C tiles of chunk k: two arrivals of mb_bc's phase.
+    // The state-only walk has two B buffers (odd chunks in the C and S tiles).
+    auto bh_off = [](int k) { return kStateOnly && (k & 1) ? kOffC : kOffBh; };
+    auto bl_off = [](int k) { return kStateOnly && (k & 1) ? kOffS : kOffBl; };
+    auto b_bar = [&](int k) { return kStateOnly && (k & 1) ? mb_g : mb_bc; };
+    auto issue_b = [&](int k) {
+        const int row = (wk.act + k) * kQ;
+        const uint32_t bar = b_bar(k);
+        tc::mbar_expect_tx(bar, 2 * kTile);
+        tc::tma_load_3d(sbase + bh_off(k), &tm_bc, 0, row, 0, bar);
+        tc::tma_load_3d(sbase + bh_off(k) + kTile / 2, &tm_bc, 64, row, 0, bar);
+        tc::tma_load_3d(sbase + bl_off(k), &tm_bc, 128, row, 0, bar);
+        tc::tma_load_3d(sbase + bl_off(k) + kTile / 2, &tm_bc, 192, row, 0, bar);
+    };
+    auto issue_c = [&](int k) {
+        const int row = (wk.act + k) * kQ;
+        tc::mbar_expect_tx(mb_bc, kTile);
+        tc::tma_load_3d(sbase + kOffC, &tm_bc, 256, row, 0, mb_bc);
+        tc::tma_load_3d(sbase + kOffC + kTile / 2, &tm_bc, 320, row, 0, mb_bc);
+    };
+
+    // helper warp: dt of both heads (adjacent: one 4-byte copy per token)
+    auto load_dt_async = [&](int k) {
+        const int cnt = tokens(k);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(sm + kOffDtBuf) + (k & 1) * kQ;
+        const __nv_bfloat16 *src = p.dt + (size_t)first_row(k) * H + 2 * hp;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 4 * lane + i;
+            if (j < cnt)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                             ::"r"(tc::smem_u32(dst + j)), "l"(src + (size_t)j * H) : "memory");
+            else
+                dst[j] = 0u;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // ---- set-up
+    if (warp == 0) tc::tmem_alloc(sbase + kOffTmem, 512);
+    if (tid == 32 * kProducerWarp) {
+        tc::prefetch_tmap(&tm_x);
+        tc::prefetch_tmap(&tm_bc);
+        if (!kStateOnly) tc::prefetch_tmap(&tm_y);
+        tc::mbar_init(mb_bc, kStateOnly ? 1 : 2);
+        tc::mbar_init(mb_x0, 1);
+        tc::mbar_init(mb_x0 + 8, 1);
+        for (uint32_t b = mb_g; b < mb_dt0; b += 8) tc::mbar_init(b, 1);
+        tc::mbar_init(mb_dt0, 32);
+        tc::mbar_init(mb_dt0 + 8, 32);
+        tc::mbar_init(mb_free0, kStateOnly ? 2 : 3);
+        tc::mbar_init(mb_free0 + 8, kStateOnly ? 2 : 3);
+        if (nk > 0) {
+            issue_x(0);
+            issue_b(0);
+            if (!kStateOnly) issue_c(0);
+        }
+        if (nk > 1) {
+            issue_x(1);
+            if (kStateOnly) issue_b(1);
+        }
+    }
+    if (warp == kHelperWarp) {
+        if (nk > 0) load_dt_async(0);
+        if (nk > 1) load_dt_async(1);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + kOffTmem);
+
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            const uint64_t dC = tc::smem_desc(sbase + kOffC, 16, 1024);    // K-major A
+            const uint64_t dBk = tc::smem_desc(sbase + kOffBh, 16, 1024);  // K-major B (G)
+            const uint64_t dS = tc::smem_desc(sbase + kOffS, 16, 1024);    // K-major B (C S^T)
+            constexpr uint32_t idG = tc::idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
+            constexpr uint32_t idY = tc::idesc_bf16(128, 64, 0, 0);
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (ok) ok = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+                return ok;
+            };
+            auto issue_g = [&]() {
+#pragma unroll 1
+                for (int ks = 0; ks < kN / 16; ++ks) {
+                    const uint32_t koff = (ks >> 2) * (kTile / 2) + (ks & 3) * 32;
+                    tc::mma_bf16(tmem + kColG, tc::desc_add(dC, koff), tc::desc_add(dBk, koff), idG, ks > 0);
+                }
+                tc::mma_commit(mb_g);
+            };
+            if (!kStateOnly && nk > 0 && wait(mb_bc, 0)) {
+                tc::fence_after_sync();
+                issue_g();
+            }
+            for (int k = 0; k < nk && ok; ++k) {
+                const uint32_t par = k & 1;
+                // S += (w o X)^T B: hi hi, lo hi, hi lo
+                if (kStateOnly) wait(b_bar(k), phase(k));
+                wait(mb_s, par);
+                if (!wait(of(mb_w0, k), phase(k))) break;
+                tc::fence_after_sync();
+                {
+                    const uint64_t dBh = tc::smem_desc(sbase + bh_off(k), kTile / 2, 1024);   // MN-major B
+                    const uint64_t dBl = tc::smem_desc(sbase + bl_off(k), kTile / 2, 1024);
+                    const uint32_t w = tmem + kColW - (kStateOnly && (k & 1) ? kColW : 0u);
+#pragma unroll 1
+                    for (int ks = 0; ks < kQ / 16; ++ks) {
+                        tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, 1);
+                        tc::mma_bf16_tmemA(tmem + kColS, w + 64 + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, 1);
+                        tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBl, ks * 2048), idS, 1);
+                    }
+                }
+                tc::mma_commit(of(mb_sd0, k));
+                if constexpr (kStateOnly) {
+                    if (k + 2 < nk && wait(of(mb_sd0, k), phase(k))) issue_b(k + 2);
+                } else {
+                    // Y = C S^T once the last chunk's rows are out of its columns
+                    if (k > 0 && !wait(mb_st, (k - 1) & 1)) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int ks = 0; ks < kN / 16; ++ks) {
+                        const uint32_t koff = (ks >> 2) * (kTile / 2) + (ks & 3) * 32;
+                        tc::mma_bf16(tmem + kColY, tc::desc_add(dC, koff), tc::desc_add(dS, koff), idG, ks > 0);
+                    }
+                    tc::mma_commit(mb_yo);
+                    // the tiles of the next chunk as soon as their last reader is done
+                    if (k + 1 < nk) {
+                        if (!wait(of(mb_sd0, k), phase(k))) break;
+                        issue_b(k + 1);
+                        if (!wait(mb_yo, par)) break;
+                        issue_c(k + 1);
+                    }
+                    wait(mb_ys, par);
+                    if (!wait(mb_m, par)) break;
+                    tc::fence_after_sync();
+                    // Y_h += M_h X_h
+                    const uint32_t xb = sbase + xbuf(k);
+#pragma unroll 1
+                    for (int ks = 0; ks < kQ / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * (kTile / 2) + (ks & 3) * 32;
+                        const uint64_t d0 = tc::smem_desc(xb, 16, 1024);
+                        tc::mma_bf16_tmemA(tmem + kColY, tmem + kColG + 16 * ks, tc::desc_add(d0, off), idY, 1);
+                        tc::mma_bf16_tmemA(tmem + kColY + 64, tmem + kColG + 16 * ks + 8,
+                                           tc::desc_add(d0, off + 64 * 128), idY, 1);
+                    }
+                    tc::mma_commit(mb_e);
+                    if (k + 1 < nk) {
+                        wait(mb_e, par);
+                        if (!wait(mb_bc, (k + 1) & 1)) break;
+                        tc::fence_after_sync();
+                        issue_g();
+                    }
+                }
+            }
+            if (!ok) record_error(p.status, kStatusTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kHelperWarp) {
+        bool ok = true;
+        const float A0 = p.A[2 * hp] * kLog2e, A1 = p.A[2 * hp + 1] * kLog2e;
+        for (int k = 0; k < nk; ++k) {
+            const int b = k & 1;
+            if (k >= 2) {
+                if (lane == 0) ok = tc::mbar_wait_bounded(mb_free0 + 8 * b, ((k >> 1) - 1) & 1, kWaitCycles);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            const __nv_bfloat162 *src = reinterpret_cast<const __nv_bfloat162 *>(sm + kOffDtBuf) + b * kQ + 4 * lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // slots 4 lane .. 4 lane + 3: prefix sums c and, for w, suffix
+                // sums c_last - c (from the end, so that the factors that
+                // matter, near the end, come from short sums)
+                const float Aw = h ? A1 : A0;
+                float d[4], a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __bfloat1622float2(src[i]);
+                    d[i] = h ? f.y : f.x;
+                    a[i] = d[i] * Aw;
+                }
+                const float own = (a[0] + a[1]) + (a[2] + a[3]);
+                float pre = own, suf = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float u = __shfl_up_sync(0xffffffffu, pre, o);
+                    const float v = __shfl_down_sync(0xffffffffu, suf, o);
+                    if (lane >= o) pre += u;
+                    if (lane + o < 32) suf += v;
+                }
+                const float all = __shfl_sync(0xffffffffu, suf, 0);
+                // (shifted, not subtracted: own may be large against the rest)
+                float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+                if (lane == 0) before = 0.0f;
+                if (lane == 31) after = 0.0f;
+                float c[4], w[4];
+                c[0] = before + a[0];
+                c[1] = c[0] + a[1];
+                c[2] = c[1] + a[2];
+                c[3] = c[2] + a[3];
+                w[3] = after;
+                w[2] = w[3] + a[3];
+                w[1] = w[2] + a[2];
+                w[0] = w[1] + a[1];
+                const int e = (b * 2 + h) * kQ + 4 * lane;
+                *reinterpret_cast<float4 *>(dts + e) = make_float4(d[0], d[1], d[2], d[3]);
+                *reinterpret_cast<float4 *>(cum + e) = make_float4(c[0], c[1], c[2], c[3]);
+                *reinterpret_cast<float4 *>(wgt + e) =
+                    make_float4(tc::exp2_approx(w[0]) * d[0], tc::exp2_approx(w[1]) * d[1],
+                                tc::exp2_approx(w[2]) * d[2], tc::exp2_approx(w[3]) * d[3]);
+                if constexpr (!kStateOnly) {
+                    *reinterpret_cast<float4 *>(f4 + e) =
+                        make_float4(tc::exp2_approx(c[3] - c[0]) * d[0], tc::exp2_approx(c[3] - c[1]) * d[1],
+                                    tc::exp2_approx(c[3] - c[2]) * d[2], d[3]);
+                    const float end = __shfl_sync(0xffffffffu, c[3], lane | 7);
+                    *reinterpret_cast<float4 *>(fB + e) =
+                        make_float4(tc::exp2_approx(end - c[0]) * d[0], tc::exp2_approx(end - c[1]) * d[1],
+                                    tc::exp2_approx(end - c[2]) * d[2], tc::exp2_approx(end - c[3]) * d[3]);
+                }
+                // exp(c_last) S as S f + (S or 0): f = exp - 1 for slow decays
+                if (lane == 0)
+                    scl[b * 2 + h] = all > -1.0f ? make_float2(expm1f(all * kLn2), all) : make_float2(exp2f(all), all);
+            }
+            if (k + 2 < nk) load_dt_async(k + 2);
+            tc::mbar_arrive(mb_dt0 + 8 * b);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (lane == 0 && !ok) record_error(p.status, kStatusTimeout);
+    } else if (warp == kPublisherWarp) {
+        if constexpr (!kStateOnly) {
+            bool ok = true;
+            for (int k = 0; k < nk; ++k) {
+                if (lane == 0) ok = tc::mbar_wait_bounded(mb_st, k & 1, kWaitCycles);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const int cnt = tokens(k), row = first_row(k);
+                if (cnt == kQ) {
+                    if (lane == 0) {
+                        const uint32_t st = sbase + xbuf(k);
+                        tc::tma_store_3d(&tm_y, st, hp * kPP, row, 0);
+                        tc::tma_store_3d(&tm_y, st + kTile / 2, hp * kPP + kP, row, 0);
+                        tc::bulk_commit();
+                        if (k + 2 < nk) {
+                            tc::bulk_wait_read0();   // the rows have been read
+                            issue_x(k + 2);
+                        }
+                    }
+                } else {
+                    // the prompt's end (always its walk's last chunk): its rows
+                    // only, 16 bytes a lane; the next rows are another prompt's
+                    const uint8_t *box = sm + xbuf(k);
+                    for (int e = lane; e < cnt * 16; e += 32) {
+                        const int r = e >> 4, h = (e >> 3) & 1, piece = e & 7;
+                        *reinterpret_cast<uint4 *>(p.y + (size_t)(row + r) * H * kP + hp * kPP + h * kP + piece * 8) =
+                            *reinterpret_cast<const uint4 *>(box + h * (kTile / 2) + tc::sw128(r, piece));
+                    }
+                }
+            }
+            if (lane == 0) {
+                tc::bulk_wait0();
+                if (!ok) record_error(p.status, kStatusTimeout);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ================= M group: thread (t = row, h) builds, for both
+        // heads, its share of M's 16-slot units in row t (M in place over G:
+        // the 16 G columns of a unit become [M_0 | M_1], 8 columns of bf16
+        // pairs each, so no other thread reads them)
+        if constexpr (!kStateOnly) {
+            const int h = tid >> 7, quad = warp & 3;
+            const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+            const float D0 = p.D[2 * hp], D1 = p.D[2 * hp + 1];
+            auto a_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+                bool w = true;
+                if (tid == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+                return grp_and(1, w);
+            };
+            bool ok = true;
+            for (int k = 0; k < nk; ++k) {
+                const int par = k & 1;
+                ok = a_wait(mb_dt0 + 8 * par, phase(k));
+                if (ok) ok = a_wait(mb_g, par);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const int row = tc::no_hoist(tid & 127);
+                // units past the row's 32-slot block are zero (s > t); of the
+                // others, warp h takes the factorised units h*quad ..
+                // h*quad+quad-1 and the diagonal unit 2 quad + h
+                {
+                    uint32_t z[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = 0u;
+#pragma unroll 1
+                    for (int U = 2 * quad + 2 + h; U < 8; U += 2)
+                        tc::tmem_st16_nw(tmem + lane_base + kColG + 16 * U, z);
+                }
+#pragma unroll 1
+                for (int iu = 0; iu <= quad; ++iu) {
+                    const int U = iu < quad ? h * quad + iu : 2 * quad + h;
+                    const int jb = U >> 1, u = U & 1;   // 32-slot block of s, half of it
+                    const uint32_t col = tmem + lane_base + kColG + 16 * U;
+                    uint32_t gu[16];
+                    tc::tmem_ld16_nw(col, gu);
+                    tc::tmem_wait_ld16(gu);
+                    const int s0 = 16 * U;
+#pragma unroll 1
+                    for (int hd = 0; hd < 2; ++hd) {
+                        const float *cm = cum + (par * 2 + hd) * kQ;
+                        const float ct = cm[row];
+                        uint32_t out[8];
+                        if (jb < quad) {
+                            // block below the diagonal: exp(c_t - c_R) exp(c_R - c_s), both <= 1
+                            const float2 *fbh = reinterpret_cast<const float2 *>(fB + (par * 2 + hd) * kQ + s0);
+                            const float et = tc::exp2_approx(ct - cm[32 * jb + 31]);
+                            const float2 et2 = make_float2(et, et);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 g2 = make_float2(__uint_as_float(gu[2 * i]), __uint_as_float(gu[2 * i + 1]));
+                                const float2 m = tc::mul2(tc::mul2(g2, et2), fbh[i]);
+                                out[i] = tc::pack_bf16x2(m.x, m.y);
+                            }
+                        } else {
+                            const int r = (row & 31) - 16 * u;   // t's place in the unit
+                            const float Dh = hd ? D1 : D0;
+                            if (cm[32 * jb] - cm[32 * jb + 31] <= 60.0f) {   // warp-uniform
+                                // through 4-slot blocks: with the whole block's decay at
+                                // most 2^60 the row factor (>= 1 inside t's own) is finite
+                                const float *f4h = f4 + (par * 2 + hd) * kQ + s0;
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4) {
+                                    const float rf = tc::exp2_approx(ct - cm[s0 + 4 * q4 + 3]);
+                                    float v[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const int i = 4 * q4 + e;
+                                        const float x = fmaf(__uint_as_float(gu[i]) * rf, f4h[i], i == r ? Dh : 0.0f);
+                                        v[e] = i <= r ? x : 0.0f;
+                                    }
+                                    out[2 * q4] = tc::pack_bf16x2(v[0], v[1]);
+                                    out[2 * q4 + 1] = tc::pack_bf16x2(v[2], v[3]);
+                                }
+                            } else {
+                                // steep decays: one exponential per element, each <= 1
+                                const float *dh = dts + (par * 2 + hd) * kQ + s0;
+#pragma unroll
+                                for (int i2 = 0; i2 < 8; ++i2) {
+                                    float v[2];
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int i = 2 * i2 + e;
+                                        const float ex = tc::exp2_approx(fminf(ct - cm[s0 + i], 0.0f));
+                                        const float x = fmaf(__uint_as_float(gu[i]) * ex, dh[i], i == r ? Dh : 0.0f);
+                                        v[e] = i <= r ? x : 0.0f;
+                                    }
+                                    out[i2] = tc::pack_bf16x2(v[0], v[1]);
+                                }
+                            }
+                        }
+                        tc::tmem_st8_nw(col + 8 * hd, out);
+                    }
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                grp_sync(1);
+                if (tid == 0) {
+                    tc::mbar_arrive(mb_m);
+                    tc::mbar_arrive(mb_free0 + 8 * par);
+                }
+            }
+            if (!ok && tid == 0) record_error(p.status, kStatusTimeout);
+        }
+    } else if (warp < 16) {
+        // ================= Y group.  State: thread (p' = row, half of n).
+        // Rows: thread (t = row, head).
+        const int tb = tid - kGroup;
+        const int hf = tb >> 7, quad = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+        auto b_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+            bool w = true;
+            if (tb == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+            return grp_and(2, w);
+        };
+        const int prow = tb & 127;
+        // this thread's 64 values of the pair's state, [head][p][n] in memory
+        const size_t pair_off = (size_t)hp * kPP * kN + (size_t)prow * kN + 64 * hf;
+        const uint32_t scol = tmem + lane_base + kColS + 64 * hf;
+        {
+            const float *from = nullptr;
+            if (!kStateOnly) {
+                if (wk.slot >= 0)
+                    from = p.seg_state + (size_t)wk.slot * H * kP * kN + pair_off;
+                else if (resume)
+                    from = p.state + (size_t)slot * H * kP * kN + pair_off;
+            }
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = from ? *reinterpret_cast<const float4 *>(from + 16 * q + 4 * i)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    r[4 * i] = __float_as_uint(v.x);
+                    r[4 * i + 1] = __float_as_uint(v.y);
+                    r[4 * i + 2] = __float_as_uint(v.z);
+                    r[4 * i + 3] = __float_as_uint(v.w);
+                }
+                tc::tmem_st16(scol + 16 * q, r);
+            }
+        }
+        // the state entering chunk k: its bf16 copy (operand of C S^T), then
+        // S <- exp(c_last) S in place
+        auto scale_state = [&](int k) {
+            const int row = tc::no_hoist(prow);
+            const float2 f = scl[(k & 1) * 2 + (quad >> 1)];
+            const bool slow = f.y > -1.0f;
+            const float2 f2 = make_float2(f.x, f.x), zero = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[16];
+                tc::tmem_ld16_nw(scol + 16 * q, r);
+                tc::tmem_wait_ld16(r);
+                if constexpr (!kStateOnly) {
+#pragma unroll
+                    for (int pc = 0; pc < 2; ++pc) {
+                        uint4 w;
+                        w.x = tc::pack_bf16x2(__uint_as_float(r[8 * pc]), __uint_as_float(r[8 * pc + 1]));
+                        w.y = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 2]), __uint_as_float(r[8 * pc + 3]));
+                        w.z = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 4]), __uint_as_float(r[8 * pc + 5]));
+                        w.w = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 6]), __uint_as_float(r[8 * pc + 7]));
+                        *reinterpret_cast<uint4 *>(sm + kOffS + hf * (kTile / 2) + tc::sw128(row, 2 * q + pc)) = w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 v = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                    const float2 o = tc::fma2(v, f2, slow ? v : zero);
+                    r[i] = __float_as_uint(o.x);
+                    r[i + 1] = __float_as_uint(o.y);
+                }
+                tc::tmem_st16_nw(scol + 16 * q, r);
+            }
+        };
+        const uint32_t ycol = tmem + lane_base + kColY + 64 * hf;
+        auto scale_rows = [&](int k) {
+            const float et = tc::exp2_approx(cum[((k & 1) * 2 + hf) * kQ + prow]);
+            const float2 et2 = make_float2(et, et);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[16];
+                tc::tmem_ld16_nw(ycol + 16 * q, r);
+                tc::tmem_wait_ld16(r);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 o = tc::mul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), et2);
+                    r[i] = __float_as_uint(o.x);
+                    r[i + 1] = __float_as_uint(o.y);
+                }
+                tc::tmem_st16_nw(ycol + 16 * q, r);
+            }
+        };
+        // chunk k's rows as two TMA store boxes (one per head: 128-byte rows,
+        // 16-byte piece j of row t at j ^ (t & 7)) in its x buffer
+        auto stage_rows = [&](int k) {
+            const int row = tc::no_hoist(prow);
+            uint8_t *box = sm + xbuf(k) + hf * (kTile / 2);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[16];
+                tc::tmem_ld16_nw(ycol + 16 * q, r);
+                tc::tmem_wait_ld16(r);
+#pragma unroll
+                for (int pc = 0; pc < 2; ++pc) {
+                    uint4 w;
+                    w.x = tc::pack_bf16x2(__uint_as_float(r[8 * pc]), __uint_as_float(r[8 * pc + 1]));
+                    w.y = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 2]), __uint_as_float(r[8 * pc + 3]));
+                    w.z = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 4]), __uint_as_float(r[8 * pc + 5]));
+                    w.w = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 6]), __uint_as_float(r[8 * pc + 7]));
+                    *reinterpret_cast<uint4 *>(box + tc::sw128(row, 2 * q + pc)) = w;
+                }
+            }
+        };
+        bool ok = true;
+        float dec = 0.0f;   // state-only: log2 of the walk's decay (this thread's head)
+        for (int k = 0; k <= nk; ++k) {
+            const int par = k & 1;
+            if (k < nk) {
+                ok = b_wait(mb_dt0 + 8 * par, phase(k));
+                // the last state product has updated S (and C S^T read the copy:
+                // waited for when its rows were scaled)
+                if (ok && k > 0) ok = b_wait(of(mb_sd0, k - 1), phase(k - 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+                scale_state(k);
+                if constexpr (kStateOnly) dec += scl[par * 2 + (quad >> 1)].y;
+                tc::tmem_wait_st();
+                if constexpr (!kStateOnly) tc::fence_proxy_async();   // the copy, for the tensor core
+                tc::fence_before_sync();
+                grp_sync(2);
+                if (tb == 0) {
+                    tc::mbar_arrive(mb_s);
+                    if (kStateOnly) tc::mbar_arrive(mb_free0 + 8 * par);
+                }
+            }
+            if constexpr (!kStateOnly) {
+                if (k > 0) {
+                    ok = b_wait(mb_e, (k - 1) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    stage_rows(k - 1);
+                    tc::fence_proxy_async();   // the rows, for the TMA store
+                    tc::fence_before_sync();   // TMEM reads before the next product writes
+                    grp_sync(2);
+                    if (tb == 0) tc::mbar_arrive(mb_st);
+                }
+                if (k < nk) {
+                    ok = b_wait(mb_yo, par);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    scale_rows(k);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    grp_sync(2);
+                    if (tb == 0) {
+                        tc::mbar_arrive(mb_ys);
+                        tc::mbar_arrive(mb_free0 + 8 * par);
+                    }
+                }
+            }
+        }
+        if (ok && nk > 0) ok = b_wait(of(mb_sd0, nk - 1), phase(nk - 1));
+        if (ok && (kStateOnly || wk.last) && (nk > 0 || !resume)) {
+            // the state after the walk (an empty prompt that resumes keeps its entry)
+            tc::fence_after_sync();
+            float *to = kStateOnly ? p.seg_state + (size_t)(wk.slot + 1) * H * kP * kN + pair_off
+                                   : p.state + (size_t)slot * H * kP * kN + pair_off;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tc::tmem_ld16(scol + 16 * q, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4 *>(to + 16 * q + 4 * i) =
+                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            if (kStateOnly && hf == 0 && (prow & 63) == 0)
+                p.seg_dec[(size_t)(wk.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
+        }
+        if (!ok && tb == 0) record_error(p.status, kStatusTimeout);
+    } else {
+        // ================= X group: thread (channel p' = lane of its quarter,
+        // half of the tokens)
+        const int tx = tid - 2 * kGroup;
+        const int hf = tx >> 7, quad = warp & 3;
+        const int pr = tx & 127;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+        const int head = quad >> 1;
+        auto c_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+            bool w = true;
+            if (tx == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+            return grp_and(3, w);
+        };
+        const int c = hp * kPP + pr;
+        const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)c * 4);
+        const float bias = p.conv_b ? p.conv_b[c] : 0.0f;
+        bool ok = true;
+        for (int k = 0; k < nk; ++k) {
+            const int par = k & 1, cnt = tokens(k);
+            // the 3 tokens before the prompt: its entry's tail, or zeros
+            const bool start = hf == 0 && k == 0 && wk.chunk == 0;
+            uint32_t r[34];   // tokens 64 hf - 3 .. 64 hf + 63 of the chunk, in pairs (the last half unused)
+            ok = c_wait(mb_x0 + 8 * par, phase(k));
+            if (!ok) break;
+            const uint8_t *raw = sm + xbuf(k) + 64 * hf * (kPP * 2) + 2 * pr;
+            auto ld = [&](int i) -> uint32_t { return *reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2)); };
+#pragma unroll
+            for (int i = 0; i < 33; ++i) r[i] = ld(2 * i) | (ld(2 * i + 1) << 16);
+            r[33] = ld(66);
+            if (start) {
+                const uint16_t *t16 = reinterpret_cast<const uint16_t *>(tail) + c;
+                const uint32_t a = resume ? t16[ch] : 0u, b = resume ? t16[2 * ch] : 0u, d = resume ? t16[3 * ch] : 0u;
+                r[0] = a | (b << 16);
+                r[1] = (r[1] & 0xffff0000u) | d;
+            }
+            // X^T replaces the raw rows once every thread has read them, and
+            // (w o X)^T the last chunk's once its product is done
+            ok = c_wait(mb_dt0 + 8 * par, phase(k));
+            if (ok) {
+                if (kStateOnly) {
+                    if (tx == 0 && k + 2 < nk) issue_x(k + 2);   // (no X^T there)
+                    if (k > 1) ok = c_wait(of(mb_sd0, k - 2), phase(k - 2));
+                } else if (k > 0) {
+                    ok = c_wait(of(mb_sd0, k - 1), phase(k - 1));
+                }
+            }
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float *ws = wgt + (par * 2 + head) * kQ + 64 * hf;
+            const uint32_t wcol = tmem + lane_base + kColW - (kStateOnly && par ? kColW : 0u) + 32 * hf;
+            uint8_t *xt = sm + xbuf(k) + hf * (kTile / 2);
+            auto val = [&](int i) { return (i & 1) ? __uint_as_float(r[i >> 1] & 0xffff0000u)
+                                                   : __uint_as_float(r[i >> 1] << 16); };
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t hi[8], lo[8], xp[8];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const int s = 16 * u + i;
+                    float a = bias, b = bias;
+                    a = fmaf(w4.x, val(s), a);
+                    a = fmaf(w4.y, val(s + 1), a);
+                    a = fmaf(w4.z, val(s + 2), a);
+                    a = fmaf(w4.w, val(s + 3), a);
+                    b = fmaf(w4.x, val(s + 1), b);
+                    b = fmaf(w4.y, val(s + 2), b);
+                    b = fmaf(w4.z, val(s + 3), b);
+                    b = fmaf(w4.w, val(s + 4), b);
+                    a = silu_approx(a);
+                    b = silu_approx(b);
+                    // tokens past the prompt's end: a neighbour's, never used
+                    if (64 * hf + s >= cnt) a = 0.0f;
+                    if (64 * hf + s + 1 >= cnt) b = 0.0f;
+                    const float2 w2 = *reinterpret_cast<const float2 *>(ws + s);
+                    xp[i >> 1] = tc::pack_bf16x2(a, b);
+                    split2(a * w2.x, b * w2.y, hi[i >> 1], lo[i >> 1]);
+                }
+                if constexpr (!kStateOnly) {
+                    *reinterpret_cast<uint4 *>(xt + tc::sw128(pr, 2 * u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
+                    *reinterpret_cast<uint4 *>(xt + tc::sw128(pr, 2 * u + 1)) = make_uint4(xp[4], xp[5], xp[6], xp[7]);
+                }
+                tc::tmem_st8_nw(wcol + 8 * u, hi);
+                tc::tmem_st8_nw(wcol + 64 + 8 * u, lo);
+            }
+            tc::tmem_wait_st();
+            if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
+            tc::fence_before_sync();
+            grp_sync(3);
+            if (tx == 0) {
+                tc::mbar_arrive(of(mb_w0, k));
+                tc::mbar_arrive(mb_free0 + 8 * par);
+            }
+        }
+        if (!ok && tx == 0) record_error(p.status, kStatusTimeout);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    if constexpr (!kStateOnly) {
+        // the new tail: by the prompt's first walk (the only one that read the
+        // old x channels; the old B and C channels were read by the prep kernel)
+        if (wk.chunk == 0) {
+            auto commit = [&](int cc) {
+                __nv_bfloat16 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = len - 4 + i;
+                    v[i] = t >= 0 ? p.xbc[(size_t)(begin + t) * ch + cc]
+                                  : resume ? tail[(size_t)(4 + t) * ch + cc] : __float2bfloat16_rn(0.0f);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tail[(size_t)i * ch + cc] = v[i];
+            };
+            if (tid < kPP) commit(hp * kPP + tid);
+            else if (hp == 0 && tid < kPP + 2 * kN) commit(H * kP + tid - kPP);
+        }
+    }
+}
+
+bool prompt_tc_supported(const bimamba_dims &d)
+{
+    return d.dtype == BIMAMBA_BF16 && d.headdim == kP && d.d_state == kN && d.ngroups == 1 && d.d_conv == 4 &&
+           d.heads % 2 == 0;
+}
+
+namespace {
+
+constexpr int kSMs = 148;
+
+struct Layout {
+    int max_chunks, seg_chunks, max_inner, max_walks, max_slots;
+    size_t head, walks, segs, act, dec, state, bytes;
+};
+
+// Sizes that hold for any lengths of `batch` prompts in `len` rows: a prompt
+// of L tokens has at most L / 128 + 1 chunks.
+Layout layout_of(const bimamba_dims &d)
+{
+    Layout l{};
+    const long long chunks = (long long)d.len / kQ + std::min(d.batch, d.len);
+    l.max_chunks = (int)chunks;
+    // A prompt is cut once it exceeds a fifth more than the GPU's average
+    // share of the call's chunks, but never below 4 chunks: the state-only
+    // walks and the chain cost about half of the walk that they let run in
+    // parallel.
+    const long long share = ((long long)d.len / kQ * (d.heads / 2) + kSMs - 1) / kSMs;
+    l.seg_chunks = (int)std::max<long long>(4, (share * 6 + 4) / 5);
+    const bool cut = d.len > l.seg_chunks * (long long)kQ;
+    l.max_inner = cut ? (int)(chunks / l.seg_chunks) : 0;
+    l.max_walks = l.max_inner + d.batch;
+    l.max_slots = 2 * l.max_inner;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return here;
+    };
+    l.head = take(sizeof(PlanHeader));
+    l.walks = take(sizeof(Walk) * (size_t)l.max_walks);
+    l.segs = take(sizeof(int2) * (size_t)d.batch);
+    l.act = take((size_t)l.max_chunks * kQ * kAct * 2);
+    l.dec = take((size_t)l.max_slots * d.heads * 4);
+    l.state = take((size_t)l.max_slots * d.heads * kP * kN * 4);
+    l.bytes = at;
+    return l;
+}
+
+// 3-D bf16 tensor map over a (rows, cols) matrix: boxes of box0 columns x box1 rows.
+bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint32_t box0, uint32_t box1,
+              bool swizzle)
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return false;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    const cuuint64_t dims[3] = {cols, rows, 1};
+    const cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+    const cuuint32_t box[3] = {box0, box1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t prompt_tc_ws_bytes(const bimamba_dims &d) { return layout_of(d).bytes; }
+
+cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
+{
+    const bimamba_dims &d = q.dims;
+    const Layout l = layout_of(d);
+    char *ws = static_cast<char *>(q.workspace);
+    PromptParams p{};
+    p.xbc = static_cast<const __nv_bfloat16 *>(q.xbc);
+    p.dt = static_cast<const __nv_bfloat16 *>(q.dt);
+    p.A = q.A; p.D = q.D; p.conv_w = q.conv_w; p.conv_b = q.conv_b;
+    p.cu = q.cu_seqlens; p.slots = q.slots; p.resume = q.resume;
+    p.state = q.state;
+    p.tail = static_cast<__nv_bfloat16 *>(q.tail);
+    p.y = static_cast<__nv_bfloat16 *>(q.y);
+    p.head = reinterpret_cast<PlanHeader *>(ws + l.head);
+    p.walks = reinterpret_cast<Walk *>(ws + l.walks);
+    p.segs = reinterpret_cast<int2 *>(ws + l.segs);
+    p.act = reinterpret_cast<__nv_bfloat16 *>(ws + l.act);
+    p.seg_dec = reinterpret_cast<float *>(ws + l.dec);
+    p.seg_state = reinterpret_cast<float *>(ws + l.state);
+    p.status = q.status;
+    p.batch = d.batch; p.len = d.len; p.H = d.heads; p.ch = d.heads * kP + 2 * kN; p.pool = q.pool;
+    p.max_chunks = l.max_chunks;
+    p.seg_chunks = l.seg_chunks;
+
+    CUtensorMap tm_x, tm_bc, tm_y;
+    // (no rows at all: the walks load nothing; the maps are placeholders)
+    const bool rows = d.len > 0;
+    const void *any = p.walks;
+    if (!make_map(&tm_x, rows ? q.xbc : any, p.ch, rows ? d.len : 1, kPP, kRawRows, false) ||
+        !make_map(&tm_bc, rows ? p.act : any, kAct, rows ? (uint64_t)l.max_chunks * kQ : 1, 64, kQ, true) ||
+        !make_map(&tm_y, rows ? q.y : any, (uint64_t)d.heads * kP, rows ? d.len : 1, kP, kQ, true))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(prompt_walk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(prompt_walk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int pairs = d.heads / 2;
+    prompt_prep_kernel<<<l.max_chunks + 1, kPrepThreads, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    count_launch();
+    if (l.max_inner > 0) {
+        prompt_walk_kernel<true><<<(unsigned)pairs * l.max_inner, kThreads, kSmemBytes, stream>>>(tm_x, tm_bc, tm_y, p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        prompt_chain_kernel<<<dim3(d.heads * kP * kN / 4 / 256, d.batch), 256, 0, stream>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        count_launch(2);
+    }
+    prompt_walk_kernel<false><<<(unsigned)pairs * l.max_walks, kThreads, kSmemBytes, stream>>>(tm_x, tm_bc, tm_y, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    count_launch();
+    return cudaSuccess;
+}
+
+}  // namespace bimamba
