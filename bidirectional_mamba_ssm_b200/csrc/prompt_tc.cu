@@ -19,9 +19,16 @@
 // tokens, so its update is not: w o X and B enter as two bf16 halves each
 // (value = hi + lo to 2^-17) and three products, hi hi + lo hi + hi lo; the
 // conv, SiLU and decays before them are fp32, exp(c_last - c_s) comes from
-// suffix sums (no cancellation where it matters), and a slow decay is applied
-// as S + S expm1(c_last), whose error does not add up over thousands of
-// chunks.
+// suffix sums (no cancellation where it matters), a slow decay is applied as
+// S + S expm1(c_last), and a chunk's products are summed on their own and
+// added once, rounding to nearest (the tensor core's sums drop what falls
+// below the accumulator's last bit: onto the state itself, thousands of such
+// steps were off by 2e-5 after 32768 tokens).  So no error adds up with the
+// number of chunks.
+//
+// A token's infinity or NaN must not reach the rows before it, but in M X it
+// meets their zeros (0 inf = NaN): such values enter X as zeros, and the rows
+// from their token on are set to NaN when they are stored.
 //
 // Kernels of one call:
 //   1. plan + conv of B and C: per 128-token chunk the operand rows
@@ -138,19 +145,41 @@ __device__ __forceinline__ int block_scan(int v, int *total)
     return before + run - v;
 }
 
-__device__ __forceinline__ float silu_approx(float a)
+__device__ __forceinline__ float rcp_approx(float v)
 {
-    // a sigmoid(a), off by a few 2^-23 (the hardware tanh's 2^-11 would do for
-    // y but not for the state)
-    return __fdividef(a, 1.0f + tc::exp2_approx(-kLog2e * a));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// a sigmoid(a) of two values, off by a few 2^-23 (the hardware tanh's 2^-11
+// would do for y but not for the state).
+__device__ __forceinline__ float2 silu2(float2 a)
+{
+    const float2 t = tc::mul2(a, make_float2(-kLog2e, -kLog2e));
+    const float2 d = tc::fma2(make_float2(tc::exp2_approx(t.x), tc::exp2_approx(t.y)), make_float2(1.0f, 1.0f),
+                              make_float2(1.0f, 1.0f));
+    return tc::mul2(a, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t v)
+{
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
 // hi = the bf16 nearest to v, lo = the bf16 nearest to v - hi, for two values.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo)
 {
-    hi = tc::pack_bf16x2(a, b);
-    const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
-    lo = tc::pack_bf16x2(ra, rb);
+    hi = tc::pack_bf16x2(v.x, v.y);
+    const float2 rest = tc::fma2(unpack2(hi), make_float2(-1.0f, -1.0f), v);
+    lo = tc::pack_bf16x2(rest.x, rest.y);
+}
+
+// Store 4 consecutive 32-bit columns of this thread's TMEM lane (no wait).
+__device__ __forceinline__ void tmem_st4_nw(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
 }  // namespace
@@ -295,8 +324,8 @@ prompt_prep_kernel(const PromptParams p)
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const bool in = t < f.w;
-                split2(in ? silu_approx(o[2 * q]) : 0.0f, in ? silu_approx(o[2 * q + 1]) : 0.0f, hi[q], lo[q]);
+                const float2 v = silu2(make_float2(o[2 * q], o[2 * q + 1]));
+                split2(t < f.w ? v : make_float2(0.0f, 0.0f), hi[q], lo[q]);
             }
             __nv_bfloat16 *row = out + (size_t)(8 * half + i) * kAct;
             if (n0 < kN) {
@@ -359,8 +388,10 @@ constexpr uint32_t kOffDt = kOffCum + kFac;         //   dt
 constexpr uint32_t kOffFB = kOffDt + kFac;          //   exp(c_R - c_s) dt_s, R = end of s's 32-slot block
 constexpr uint32_t kOffF4 = kOffFB + kFac;          //   exp(c_R4 - c_s) dt_s, R4 = s | 3
 constexpr uint32_t kOffWgt = kOffF4 + kFac;         //   w_s
-constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]: see scale_state
-constexpr uint32_t kOffDtBuf = kOffScale + 32;      // [2][128] bf16x2: dt of both heads
+constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]: see next_state
+constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][256]: first token of X not finite (128: none)
+constexpr uint32_t kOffAnyBad = kOffBad + 512;      // int [2 parity]
+constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
 constexpr uint32_t kOffMbar = kOffDtBuf + 2 * kQ * 4;
 constexpr uint32_t kOffTmem = kOffMbar + 160;
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
@@ -372,14 +403,49 @@ static_assert(kRawBytes <= kXbufBytes && kSmemBytes <= 227 * 1024, "shared memor
 constexpr uint32_t kColG = 0;      // G, then in place [M_0 | M_1] per 16 tokens (8 + 8 columns of bf16 pairs)
 constexpr uint32_t kColY = 128;    // Y, 64 columns per head
 constexpr uint32_t kColW = 256;    // (w o X)^T, A operand: 64 columns hi, 64 columns lo
-constexpr uint32_t kColS = 384;    // S [p' = lane][n], fp32
+constexpr uint32_t kColS = 384;    // a chunk's (w o X)^T B [p' = lane][n], fp32
 
-// ---- warps: three groups of 8 and three single ones
+// ---- warps: three groups of 8 and three single ones (a fourth is idle: the
+// register shares below are given to whole sets of 4 warps)
 constexpr int kGroup = 256;
 constexpr int kProducerWarp = 24, kHelperWarp = 25, kPublisherWarp = 26;
-constexpr int kThreads = 27 * 32;
+constexpr int kThreads = 28 * 32;
+// registers a thread: 896 threads are launched with 72; the Y group holds the
+// state (64 values a thread) and the X group its channel's raw tokens
+constexpr int kRegsLaunch = 72, kRegsM = 56, kRegsY = 96, kRegsX = 80, kRegsOne = 40;
+static_assert((kRegsM + kRegsY + kRegsX) * kGroup + kRegsOne * 128 <= kRegsLaunch * kThreads, "register shares");
+
+template <int kRegs> __device__ __forceinline__ void take_registers()
+{
+    if constexpr (kRegs == kRegsLaunch)
+        return;
+    else if constexpr (kRegs > kRegsLaunch)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 
 __device__ __forceinline__ void grp_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+__device__ __forceinline__ bool grp_or(int id, bool pred)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "bar.red.or.pred q, %1, 256, p;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"((uint32_t)pred) : "memory");
+    return r != 0;
+}
 
 __device__ __forceinline__ bool grp_and(int id, bool pred)
 {
@@ -401,9 +467,9 @@ __device__ __forceinline__ bool grp_and(int id, bool pred)
 // Warp roles (hand-offs through mbarriers, every wait bounded; [k] = once
 // per chunk):
 //   warps 0..7   M group: M(k) in place over G(k).
-//   warps 8..15  Y group: the state scaled for chunk k with its bf16 copy;
-//                the rows of C S^T scaled by exp(c_t) in place, ready for M X
-//                to be added; the finished rows to the chunk's x buffer.
+//   warps 8..15  Y group: the state (in registers) and its bf16 copy; the rows
+//                of C S^T scaled by exp(c_t) in place, ready for M X to be
+//                added; the finished rows to the chunk's x buffer.
 //   warps 16..23 X group: conv + SiLU of the chunk's raw rows; X^T in place in
 //                the x buffer, both halves of (w o X)^T to tensor memory.
 //                (lane = channel, so that a thread's tokens are consecutive:
@@ -447,12 +513,14 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     float *f4 = reinterpret_cast<float *>(sm + kOffF4);
     float *wgt = reinterpret_cast<float *>(sm + kOffWgt);
     float2 *scl = reinterpret_cast<float2 *>(sm + kOffScale);
+    uint8_t *bad_at = sm + kOffBad;
+    int *any_bad = reinterpret_cast<int *>(sm + kOffAnyBad);
     const uint32_t mb = sbase + kOffMbar;
     const uint32_t mb_bc = mb;            // [k] B/C tiles landed (state-only: even chunks, odd ones at mb_g)
     const uint32_t mb_x0 = mb + 8;        // raw x landed in buffer k % 2 (+8)
     const uint32_t mb_g = mb + 24;        // [k] G done
     const uint32_t mb_m = mb + 32;        // [k] M ready
-    const uint32_t mb_s = mb + 40;        // [k] state scaled, its copy ready
+    const uint32_t mb_s = mb + 40;        // [k] the copy of the state entering it ready, kColS read
     const uint32_t mb_yo = mb + 48;       // [k] C S^T done
     const uint32_t mb_ys = mb + 56;       // [k] its rows scaled
     const uint32_t mb_e = mb + 64;        // [k] M X done
@@ -546,93 +614,115 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     tc::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + kOffTmem);
 
+    if (warp >= kProducerWarp) take_registers<kRegsOne>();
     if (warp == kProducerWarp) {
-        if (lane == 0) {
-            const uint64_t dC = tc::smem_desc(sbase + kOffC, 16, 1024);    // K-major A
-            const uint64_t dBk = tc::smem_desc(sbase + kOffBh, 16, 1024);  // K-major B (G)
-            const uint64_t dS = tc::smem_desc(sbase + kOffS, 16, 1024);    // K-major B (C S^T)
-            constexpr uint32_t idG = tc::idesc_bf16(128, 128, 0, 0);
-            constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
-            constexpr uint32_t idY = tc::idesc_bf16(128, 64, 0, 0);
-            bool ok = true;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (ok) ok = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-                return ok;
-            };
-            auto issue_g = [&]() {
-#pragma unroll 1
-                for (int ks = 0; ks < kN / 16; ++ks) {
-                    const uint32_t koff = (ks >> 2) * (kTile / 2) + (ks & 3) * 32;
-                    tc::mma_bf16(tmem + kColG, tc::desc_add(dC, koff), tc::desc_add(dBk, koff), idG, ks > 0);
-                }
+        // the whole warp follows the loop, one elected lane issues: what the
+        // MMAs take then stays in uniform registers
+        const bool issuer = elect_one();
+        const uint64_t dC = tc::smem_desc(sbase + kOffC, 16, 1024);    // K-major A
+        const uint64_t dBk = tc::smem_desc(sbase + kOffBh, 16, 1024);  // K-major B (G)
+        const uint64_t dS = tc::smem_desc(sbase + kOffS, 16, 1024);    // K-major B (C S^T)
+        constexpr uint32_t idG = tc::idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
+        constexpr uint32_t idY = tc::idesc_bf16(128, 64, 0, 0);
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (ok) ok = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+            return ok;
+        };
+        // a wait that gave up in one lane gives up in all
+        auto all_ok = [&]() { return ok = __all_sync(0xffffffffu, ok); };
+        auto koff = [](int ks) -> uint32_t { return (ks >> 2) * (kTile / 2) + (ks & 3) * 32; };   // K-major step
+        auto issue_g = [&]() {
+            if (issuer) {
+#pragma unroll
+                for (int ks = 0; ks < kN / 16; ++ks)
+                    tc::mma_bf16(tmem + kColG, tc::desc_add(dC, koff(ks)), tc::desc_add(dBk, koff(ks)), idG, ks > 0);
                 tc::mma_commit(mb_g);
-            };
-            if (!kStateOnly && nk > 0 && wait(mb_bc, 0)) {
+            }
+            __syncwarp();
+        };
+        if (!kStateOnly && nk > 0) {
+            wait(mb_bc, 0);
+            if (all_ok()) {
                 tc::fence_after_sync();
                 issue_g();
             }
-            for (int k = 0; k < nk && ok; ++k) {
-                const uint32_t par = k & 1;
-                // S += (w o X)^T B: hi hi, lo hi, hi lo
-                if (kStateOnly) wait(b_bar(k), phase(k));
-                wait(mb_s, par);
-                if (!wait(of(mb_w0, k), phase(k))) break;
-                tc::fence_after_sync();
-                {
-                    const uint64_t dBh = tc::smem_desc(sbase + bh_off(k), kTile / 2, 1024);   // MN-major B
-                    const uint64_t dBl = tc::smem_desc(sbase + bl_off(k), kTile / 2, 1024);
-                    const uint32_t w = tmem + kColW - (kStateOnly && (k & 1) ? kColW : 0u);
-#pragma unroll 1
-                    for (int ks = 0; ks < kQ / 16; ++ks) {
-                        tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, 1);
-                        tc::mma_bf16_tmemA(tmem + kColS, w + 64 + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, 1);
-                        tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBl, ks * 2048), idS, 1);
-                    }
+        }
+        for (int k = 0; k < nk && ok; ++k) {
+            const uint32_t par = k & 1;
+            // (w o X)^T B: hi hi, lo hi, hi lo
+            if (kStateOnly) wait(b_bar(k), phase(k));
+            wait(mb_s, par);
+            wait(of(mb_w0, k), phase(k));
+            if (!all_ok()) break;
+            tc::fence_after_sync();
+            if (issuer) {
+                const uint64_t dBh = tc::smem_desc(sbase + bh_off(k), kTile / 2, 1024);   // MN-major B
+                const uint64_t dBl = tc::smem_desc(sbase + bl_off(k), kTile / 2, 1024);
+                const uint32_t w = tmem + kColW - (kStateOnly && (k & 1) ? kColW : 0u);
+#pragma unroll
+                for (int ks = 0; ks < kQ / 16; ++ks) {
+                    tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, ks > 0);
+                    tc::mma_bf16_tmemA(tmem + kColS, w + 64 + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, 1);
+                    tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBl, ks * 2048), idS, 1);
                 }
                 tc::mma_commit(of(mb_sd0, k));
-                if constexpr (kStateOnly) {
-                    if (k + 2 < nk && wait(of(mb_sd0, k), phase(k))) issue_b(k + 2);
-                } else {
-                    // Y = C S^T once the last chunk's rows are out of its columns
-                    if (k > 0 && !wait(mb_st, (k - 1) & 1)) break;
-                    tc::fence_after_sync();
-#pragma unroll 1
-                    for (int ks = 0; ks < kN / 16; ++ks) {
-                        const uint32_t koff = (ks >> 2) * (kTile / 2) + (ks & 3) * 32;
-                        tc::mma_bf16(tmem + kColY, tc::desc_add(dC, koff), tc::desc_add(dS, koff), idG, ks > 0);
-                    }
+            }
+            __syncwarp();
+            if constexpr (kStateOnly) {
+                if (k + 2 < nk) {
+                    wait(of(mb_sd0, k), phase(k));
+                    if (!all_ok()) break;
+                    if (issuer) issue_b(k + 2);
+                }
+            } else {
+                // Y = C S^T once the last chunk's rows are out of its columns
+                if (k > 0) wait(mb_st, (k - 1) & 1);
+                if (!all_ok()) break;
+                tc::fence_after_sync();
+                if (issuer) {
+#pragma unroll
+                    for (int ks = 0; ks < kN / 16; ++ks)
+                        tc::mma_bf16(tmem + kColY, tc::desc_add(dC, koff(ks)), tc::desc_add(dS, koff(ks)), idG, ks > 0);
                     tc::mma_commit(mb_yo);
-                    // the tiles of the next chunk as soon as their last reader is done
-                    if (k + 1 < nk) {
-                        if (!wait(of(mb_sd0, k), phase(k))) break;
-                        issue_b(k + 1);
-                        if (!wait(mb_yo, par)) break;
-                        issue_c(k + 1);
-                    }
-                    wait(mb_ys, par);
-                    if (!wait(mb_m, par)) break;
-                    tc::fence_after_sync();
-                    // Y_h += M_h X_h
-                    const uint32_t xb = sbase + xbuf(k);
-#pragma unroll 1
+                }
+                __syncwarp();
+                // the tiles of the next chunk as soon as their last reader is done
+                if (k + 1 < nk) {
+                    wait(of(mb_sd0, k), phase(k));
+                    if (!all_ok()) break;
+                    if (issuer) issue_b(k + 1);
+                    wait(mb_yo, par);
+                    if (!all_ok()) break;
+                    if (issuer) issue_c(k + 1);
+                }
+                wait(mb_ys, par);
+                wait(mb_m, par);
+                if (!all_ok()) break;
+                tc::fence_after_sync();
+                // Y_h += M_h X_h
+                if (issuer) {
+                    const uint64_t d0 = tc::smem_desc(sbase + xbuf(k), 16, 1024);
+#pragma unroll
                     for (int ks = 0; ks < kQ / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * (kTile / 2) + (ks & 3) * 32;
-                        const uint64_t d0 = tc::smem_desc(xb, 16, 1024);
-                        tc::mma_bf16_tmemA(tmem + kColY, tmem + kColG + 16 * ks, tc::desc_add(d0, off), idY, 1);
+                        tc::mma_bf16_tmemA(tmem + kColY, tmem + kColG + 16 * ks, tc::desc_add(d0, koff(ks)), idY, 1);
                         tc::mma_bf16_tmemA(tmem + kColY + 64, tmem + kColG + 16 * ks + 8,
-                                           tc::desc_add(d0, off + 64 * 128), idY, 1);
+                                           tc::desc_add(d0, koff(ks) + 64 * 128), idY, 1);
                     }
                     tc::mma_commit(mb_e);
-                    if (k + 1 < nk) {
-                        wait(mb_e, par);
-                        if (!wait(mb_bc, (k + 1) & 1)) break;
-                        tc::fence_after_sync();
-                        issue_g();
-                    }
+                }
+                __syncwarp();
+                if (k + 1 < nk) {
+                    wait(mb_e, par);
+                    wait(mb_bc, (k + 1) & 1);
+                    if (!all_ok()) break;
+                    tc::fence_after_sync();
+                    issue_g();
                 }
             }
-            if (!ok) record_error(p.status, kStatusTimeout);
         }
+        if (!ok && lane == 0) record_error(p.status, kStatusTimeout);
         __syncwarp();
     } else if (warp == kHelperWarp) {
         bool ok = true;
@@ -748,6 +838,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // heads, its share of M's 16-slot units in row t (M in place over G:
         // the 16 G columns of a unit become [M_0 | M_1], 8 columns of bf16
         // pairs each, so no other thread reads them)
+        take_registers<kRegsM>();
         if constexpr (!kStateOnly) {
             const int h = tid >> 7, quad = warp & 3;
             const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
@@ -785,7 +876,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::tmem_ld16_nw(col, gu);
                     tc::tmem_wait_ld16(gu);
                     const int s0 = 16 * U;
-#pragma unroll 1
+#pragma unroll
                     for (int hd = 0; hd < 2; ++hd) {
                         const float *cm = cum + (par * 2 + hd) * kQ;
                         const float ct = cm[row];
@@ -852,8 +943,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (!ok && tid == 0) record_error(p.status, kStatusTimeout);
         }
     } else if (warp < 16) {
-        // ================= Y group.  State: thread (p' = row, half of n).
-        // Rows: thread (t = row, head).
+        // ================= Y group.  State: thread (p' = row, half of n), its
+        // 64 values in registers.  Rows: thread (t = row, head).
+        take_registers<kRegsY>();
         const int tb = tid - kGroup;
         const int hf = tb >> 7, quad = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
@@ -863,9 +955,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             return grp_and(2, w);
         };
         const int prow = tb & 127;
-        // this thread's 64 values of the pair's state, [head][p][n] in memory
+        // this thread's values of the pair's state, [head][p][n] in memory
         const size_t pair_off = (size_t)hp * kPP * kN + (size_t)prow * kN + 64 * hf;
         const uint32_t scol = tmem + lane_base + kColS + 64 * hf;
+        float2 st[32];
         {
             const float *from = nullptr;
             if (!kStateOnly) {
@@ -874,52 +967,44 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 else if (resume)
                     from = p.state + (size_t)slot * H * kP * kN + pair_off;
             }
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                uint32_t r[16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 v = from ? *reinterpret_cast<const float4 *>(from + 16 * q + 4 * i)
-                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    r[4 * i] = __float_as_uint(v.x);
-                    r[4 * i + 1] = __float_as_uint(v.y);
-                    r[4 * i + 2] = __float_as_uint(v.z);
-                    r[4 * i + 3] = __float_as_uint(v.w);
-                }
-                tc::tmem_st16(scol + 16 * q, r);
+            for (int i = 0; i < 16; ++i) {
+                const float4 v = from ? *reinterpret_cast<const float4 *>(from + 4 * i)
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                st[2 * i] = make_float2(v.x, v.y);
+                st[2 * i + 1] = make_float2(v.z, v.w);
             }
         }
-        // the state entering chunk k: its bf16 copy (operand of C S^T), then
-        // S <- exp(c_last) S in place
-        auto scale_state = [&](int k) {
-            const int row = tc::no_hoist(prow);
+        float dec = 0.0f;   // state-only: log2 of the walk's decay (this thread's head)
+        // S <- exp(c_last) S + chunk k's products
+        auto next_state = [&](int k) {
             const float2 f = scl[(k & 1) * 2 + (quad >> 1)];
             const bool slow = f.y > -1.0f;
-            const float2 f2 = make_float2(f.x, f.x), zero = make_float2(0.0f, 0.0f);
-#pragma unroll 1
+            const float2 f2 = make_float2(f.x, f.x), zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
+            if constexpr (kStateOnly) dec += f.y;
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t r[16];
                 tc::tmem_ld16_nw(scol + 16 * q, r);
                 tc::tmem_wait_ld16(r);
-                if constexpr (!kStateOnly) {
 #pragma unroll
-                    for (int pc = 0; pc < 2; ++pc) {
-                        uint4 w;
-                        w.x = tc::pack_bf16x2(__uint_as_float(r[8 * pc]), __uint_as_float(r[8 * pc + 1]));
-                        w.y = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 2]), __uint_as_float(r[8 * pc + 3]));
-                        w.z = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 4]), __uint_as_float(r[8 * pc + 5]));
-                        w.w = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 6]), __uint_as_float(r[8 * pc + 7]));
-                        *reinterpret_cast<uint4 *>(sm + kOffS + hf * (kTile / 2) + tc::sw128(row, 2 * q + pc)) = w;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    float2 &v = st[8 * q + i];
+                    v = tc::fma2(v, f2, slow ? v : zero);
+                    v = tc::fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), one, v);
                 }
+            }
+        };
+        // the bf16 copy of the state (operand of C S^T)
+        auto copy_state = [&]() {
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float2 v = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-                    const float2 o = tc::fma2(v, f2, slow ? v : zero);
-                    r[i] = __float_as_uint(o.x);
-                    r[i + 1] = __float_as_uint(o.y);
-                }
-                tc::tmem_st16_nw(scol + 16 * q, r);
+            for (int pc = 0; pc < 8; ++pc) {
+                uint4 w;
+                w.x = tc::pack_bf16x2(st[4 * pc].x, st[4 * pc].y);
+                w.y = tc::pack_bf16x2(st[4 * pc + 1].x, st[4 * pc + 1].y);
+                w.z = tc::pack_bf16x2(st[4 * pc + 2].x, st[4 * pc + 2].y);
+                w.w = tc::pack_bf16x2(st[4 * pc + 3].x, st[4 * pc + 3].y);
+                *reinterpret_cast<uint4 *>(sm + kOffS + hf * (kTile / 2) + tc::sw128(prow, pc)) = w;
             }
         };
         const uint32_t ycol = tmem + lane_base + kColY + 64 * hf;
@@ -945,11 +1030,18 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         auto stage_rows = [&](int k) {
             const int row = tc::no_hoist(prow);
             uint8_t *box = sm + xbuf(k) + hf * (kTile / 2);
+            const bool bad = any_bad[k & 1] != 0;   // (rare: see the top)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t r[16];
                 tc::tmem_ld16_nw(ycol + 16 * q, r);
                 tc::tmem_wait_ld16(r);
+                if (bad) {
+                    const uint8_t *b = bad_at + (k & 1) * 256 + 64 * hf + 16 * q;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (row >= min(b[i], b[128 + i])) r[i] = 0x7fffffffu;
+                }
 #pragma unroll
                 for (int pc = 0; pc < 2; ++pc) {
                     uint4 w;
@@ -962,26 +1054,29 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
         };
         bool ok = true;
-        float dec = 0.0f;   // state-only: log2 of the walk's decay (this thread's head)
         for (int k = 0; k <= nk; ++k) {
             const int par = k & 1;
-            if (k < nk) {
-                ok = b_wait(mb_dt0 + 8 * par, phase(k));
-                // the last state product has updated S (and C S^T read the copy:
-                // waited for when its rows were scaled)
-                if (ok && k > 0) ok = b_wait(of(mb_sd0, k - 1), phase(k - 1));
+            if (k > 0) {
+                // (factors of chunk k - 1: waited for when its rows were scaled)
+                ok = b_wait(of(mb_sd0, k - 1), phase(k - 1));
                 if (!ok) break;
                 tc::fence_after_sync();
-                scale_state(k);
-                if constexpr (kStateOnly) dec += scl[par * 2 + (quad >> 1)].y;
-                tc::tmem_wait_st();
-                if constexpr (!kStateOnly) tc::fence_proxy_async();   // the copy, for the tensor core
-                tc::fence_before_sync();
+                next_state(k - 1);
+            }
+            if (k < nk) {
+                // (C S^T of the last chunk has read the copy: waited for too)
+                if constexpr (!kStateOnly) {
+                    copy_state();
+                    tc::fence_proxy_async();   // the copy, for the tensor core
+                }
+                tc::fence_before_sync();       // the reads of kColS before the next products
                 grp_sync(2);
                 if (tb == 0) {
                     tc::mbar_arrive(mb_s);
-                    if (kStateOnly) tc::mbar_arrive(mb_free0 + 8 * par);
+                    if (k > 0) tc::mbar_arrive(of(mb_free0, k - 1));
                 }
+                if (kStateOnly) ok = b_wait(of(mb_dt0, k), phase(k));
+                if (!ok) break;
             }
             if constexpr (!kStateOnly) {
                 if (k > 0) {
@@ -995,42 +1090,34 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     if (tb == 0) tc::mbar_arrive(mb_st);
                 }
                 if (k < nk) {
-                    ok = b_wait(mb_yo, par);
+                    ok = b_wait(of(mb_dt0, k), phase(k));
+                    if (ok) ok = b_wait(mb_yo, par);
                     if (!ok) break;
                     tc::fence_after_sync();
                     scale_rows(k);
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     grp_sync(2);
-                    if (tb == 0) {
-                        tc::mbar_arrive(mb_ys);
-                        tc::mbar_arrive(mb_free0 + 8 * par);
-                    }
+                    if (tb == 0) tc::mbar_arrive(mb_ys);
                 }
             }
         }
-        if (ok && nk > 0) ok = b_wait(of(mb_sd0, nk - 1), phase(nk - 1));
         if (ok && (kStateOnly || wk.last) && (nk > 0 || !resume)) {
             // the state after the walk (an empty prompt that resumes keeps its entry)
-            tc::fence_after_sync();
             float *to = kStateOnly ? p.seg_state + (size_t)(wk.slot + 1) * H * kP * kN + pair_off
                                    : p.state + (size_t)slot * H * kP * kN + pair_off;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                float v[16];
-                tc::tmem_ld16(scol + 16 * q, v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float4 *>(to + 16 * q + 4 * i) =
-                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            }
+            for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<float4 *>(to + 4 * i) =
+                    make_float4(st[2 * i].x, st[2 * i].y, st[2 * i + 1].x, st[2 * i + 1].y);
             if (kStateOnly && hf == 0 && (prow & 63) == 0)
                 p.seg_dec[(size_t)(wk.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
         }
         if (!ok && tb == 0) record_error(p.status, kStatusTimeout);
-    } else {
+    } else if (warp < kProducerWarp) {
         // ================= X group: thread (channel p' = lane of its quarter,
         // half of the tokens)
+        take_registers<kRegsX>();
         const int tx = tid - 2 * kGroup;
         const int hf = tx >> 7, quad = warp & 3;
         const int pr = tx & 127;
@@ -1047,17 +1134,28 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         bool ok = true;
         for (int k = 0; k < nk; ++k) {
             const int par = k & 1, cnt = tokens(k);
-            // the 3 tokens before the prompt: its entry's tail, or zeros
-            const bool start = hf == 0 && k == 0 && wk.chunk == 0;
             uint32_t r[34];   // tokens 64 hf - 3 .. 64 hf + 63 of the chunk, in pairs (the last half unused)
             ok = c_wait(mb_x0 + 8 * par, phase(k));
             if (!ok) break;
-            const uint8_t *raw = sm + xbuf(k) + 64 * hf * (kPP * 2) + 2 * pr;
-            auto ld = [&](int i) -> uint32_t { return *reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2)); };
+            {
+                const uint8_t *raw = sm + xbuf(k) + 64 * hf * (kPP * 2) + 2 * pr;
+                auto ld = [&](int i) -> uint32_t { return *reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2)); };
 #pragma unroll
-            for (int i = 0; i < 33; ++i) r[i] = ld(2 * i) | (ld(2 * i + 1) << 16);
-            r[33] = ld(66);
-            if (start) {
+                for (int i = 0; i < 33; ++i) r[i] = ld(2 * i) | (ld(2 * i + 1) << 16);
+                r[33] = ld(66);
+            }
+            if (cnt < kQ) {
+                // tokens past the prompt's end are a neighbour's: zeros (what
+                // the conv makes of them meets dt = 0 and M = 0)
+                const int left = cnt - 64 * hf + 3;   // values of r that are this prompt's
+#pragma unroll
+                for (int i = 0; i < 34; ++i) {
+                    if (2 * i >= left) r[i] = 0u;
+                    else if (2 * i + 1 >= left) r[i] &= 0xffffu;
+                }
+            }
+            if (hf == 0 && k == 0 && wk.chunk == 0) {
+                // the 3 tokens before the prompt: its entry's tail, or zeros
                 const uint16_t *t16 = reinterpret_cast<const uint16_t *>(tail) + c;
                 const uint32_t a = resume ? t16[ch] : 0u, b = resume ? t16[2 * ch] : 0u, d = resume ? t16[3 * ch] : 0u;
                 r[0] = a | (b << 16);
@@ -1065,7 +1163,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
             // X^T replaces the raw rows once every thread has read them, and
             // (w o X)^T the last chunk's once its product is done
-            ok = c_wait(mb_dt0 + 8 * par, phase(k));
+            ok = c_wait(of(mb_dt0, k), phase(k));
             if (ok) {
                 if (kStateOnly) {
                     if (tx == 0 && k + 2 < nk) issue_x(k + 2);   // (no X^T there)
@@ -1079,44 +1177,64 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             const float *ws = wgt + (par * 2 + head) * kQ + 64 * hf;
             const uint32_t wcol = tmem + lane_base + kColW - (kStateOnly && par ? kColW : 0u) + 32 * hf;
             uint8_t *xt = sm + xbuf(k) + hf * (kTile / 2);
-            auto val = [&](int i) { return (i & 1) ? __uint_as_float(r[i >> 1] & 0xffff0000u)
-                                                   : __uint_as_float(r[i >> 1] << 16); };
+            const float2 wa = make_float2(w4.x, w4.x), wb = make_float2(w4.y, w4.y), wc = make_float2(w4.z, w4.z),
+                         wd = make_float2(w4.w, w4.w), b2 = make_float2(bias, bias);
+            // packed pairs of consecutive tokens: even ones are a word of r,
+            // odd ones straddle two
+            auto odd = [&](int i) { return make_float2(__uint_as_float(r[i] & 0xffff0000u), __uint_as_float(r[i + 1] << 16)); };
+            __nv_bfloat162 check = __float2bfloat162_rn(0.0f);   // NaN once an activation is not finite
+            float2 e0 = unpack2(r[0]), o0 = odd(0);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t hi[8], lo[8], xp[8];
+            for (int u = 0; u < 8; ++u) {
+                uint32_t hi[4], lo[4], xp[4];
+                const float4 w01 = *reinterpret_cast<const float4 *>(ws + 8 * u);
+                const float4 w23 = *reinterpret_cast<const float4 *>(ws + 8 * u + 4);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const int s = 16 * u + i;
-                    float a = bias, b = bias;
-                    a = fmaf(w4.x, val(s), a);
-                    a = fmaf(w4.y, val(s + 1), a);
-                    a = fmaf(w4.z, val(s + 2), a);
-                    a = fmaf(w4.w, val(s + 3), a);
-                    b = fmaf(w4.x, val(s + 1), b);
-                    b = fmaf(w4.y, val(s + 2), b);
-                    b = fmaf(w4.z, val(s + 3), b);
-                    b = fmaf(w4.w, val(s + 4), b);
-                    a = silu_approx(a);
-                    b = silu_approx(b);
-                    // tokens past the prompt's end: a neighbour's, never used
-                    if (64 * hf + s >= cnt) a = 0.0f;
-                    if (64 * hf + s + 1 >= cnt) b = 0.0f;
-                    const float2 w2 = *reinterpret_cast<const float2 *>(ws + s);
-                    xp[i >> 1] = tc::pack_bf16x2(a, b);
-                    split2(a * w2.x, b * w2.y, hi[i >> 1], lo[i >> 1]);
+                for (int j = 0; j < 4; ++j) {
+                    const int i = 4 * u + j;   // tokens 2 i, 2 i + 1
+                    const float2 e1 = unpack2(r[i + 1]), o1 = odd(i + 1 < 33 ? i + 1 : 32);
+                    float2 a = tc::fma2(wa, e0, b2);
+                    a = tc::fma2(wb, o0, a);
+                    a = tc::fma2(wc, e1, a);
+                    a = tc::fma2(wd, o1, a);
+                    const float2 x = silu2(a);
+                    if constexpr (!kStateOnly) {
+                        xp[j] = tc::pack_bf16x2(x.x, x.y);
+                        check = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&xp[j]), __float2bfloat162_rn(0.0f),
+                                        check);
+                    }
+                    const float2 w = j == 0 ? make_float2(w01.x, w01.y) : j == 1 ? make_float2(w01.z, w01.w)
+                                   : j == 2 ? make_float2(w23.x, w23.y) : make_float2(w23.z, w23.w);
+                    split2(tc::mul2(x, w), hi[j], lo[j]);
+                    e0 = e1;
+                    o0 = o1;
                 }
-                if constexpr (!kStateOnly) {
-                    *reinterpret_cast<uint4 *>(xt + tc::sw128(pr, 2 * u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
-                    *reinterpret_cast<uint4 *>(xt + tc::sw128(pr, 2 * u + 1)) = make_uint4(xp[4], xp[5], xp[6], xp[7]);
+                if constexpr (!kStateOnly)
+                    *reinterpret_cast<uint4 *>(xt + tc::sw128(pr, u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
+                tmem_st4_nw(wcol + 4 * u, hi);
+                tmem_st4_nw(wcol + 64 + 4 * u, lo);
+            }
+            bool bad = false;
+            if constexpr (!kStateOnly) {
+                bad = !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
+                int at = kQ;
+                if (bad) {
+                    for (int i = 63; i >= 0; --i) {
+                        uint16_t *v = reinterpret_cast<uint16_t *>(xt + tc::sw128(pr, i >> 3)) + (i & 7);
+                        if ((*v & 0x7f80u) == 0x7f80u) {
+                            *v = 0;
+                            at = 64 * hf + i;
+                        }
+                    }
                 }
-                tc::tmem_st8_nw(wcol + 8 * u, hi);
-                tc::tmem_st8_nw(wcol + 64 + 8 * u, lo);
+                bad_at[par * 256 + tx] = (uint8_t)at;
             }
             tc::tmem_wait_st();
             if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
             tc::fence_before_sync();
-            grp_sync(3);
+            bad = grp_or(3, bad);
             if (tx == 0) {
+                any_bad[par] = bad;
                 tc::mbar_arrive(of(mb_w0, k));
                 tc::mbar_arrive(mb_free0 + 8 * par);
             }
