@@ -376,12 +376,12 @@ namespace {
 constexpr uint32_t kTile = 32768;                   // 128 x 128 bf16: two 64-wide swizzled blocks
 constexpr uint32_t kOffC = 0;                       // C  [t][n]
 constexpr uint32_t kOffBh = kOffC + kTile;          // B hi [s][n]
-constexpr uint32_t kOffBl = kOffBh + kTile;         // B lo [s][n]
-constexpr uint32_t kXbufBytes = 33792;              // raw x [131][128] -> X^T [p'][s] -> output rows
-constexpr uint32_t kOffX0 = kOffBl + kTile;         // even chunks
-constexpr uint32_t kOffX1 = kOffX0 + kXbufBytes;    // odd chunks
-constexpr uint32_t kOffS = kOffX1 + kXbufBytes;     // bf16 copy of the state [p'][n]
-constexpr uint32_t kOffFac = kOffS + kTile;         // per-slot factors, f32 [2 parity][2 head][128] each:
+constexpr uint32_t kOffBl = kOffBh + kTile;         // B lo [s][n], then the bf16 copy of the state [p'][n]
+constexpr uint32_t kOffX0 = kOffBl + kTile;         // X^T [p'][s], then the finished rows: even chunks
+constexpr uint32_t kOffX1 = kOffX0 + kTile;         // odd chunks
+constexpr uint32_t kOffRaw = kOffX1 + kTile;        // raw x [131][128]
+constexpr uint32_t kRawBytes = kRawRows * kPP * 2;
+constexpr uint32_t kOffFac = kOffRaw + kRawBytes;   // per-slot factors, f32 [2 parity][2 head][128] each:
 constexpr uint32_t kFac = 2 * 2 * kQ * 4;
 constexpr uint32_t kOffCum = kOffFac;               //   prefix sums of dt A, log2 units
 constexpr uint32_t kOffDt = kOffCum + kFac;         //   dt
@@ -389,15 +389,14 @@ constexpr uint32_t kOffFB = kOffDt + kFac;          //   exp(c_R - c_s) dt_s, R 
 constexpr uint32_t kOffF4 = kOffFB + kFac;          //   exp(c_R4 - c_s) dt_s, R4 = s | 3
 constexpr uint32_t kOffWgt = kOffF4 + kFac;         //   w_s
 constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]: see next_state
-constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][256]: first token of X not finite (128: none)
-constexpr uint32_t kOffAnyBad = kOffBad + 512;      // int [2 parity]
+constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][3][128]: first token of X not finite (128: none)
+constexpr uint32_t kOffAnyBad = kOffBad + 768;      // int [2 parity]
 constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
 constexpr uint32_t kOffMbar = kOffDtBuf + 2 * kQ * 4;
 constexpr uint32_t kOffTmem = kOffMbar + 160;
+
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
-constexpr uint32_t kRawBytes = kRawRows * kPP * 2;
-static_assert(kOffX0 % 1024 == 0 && kOffX1 % 1024 == 0 && kOffS % 1024 == 0, "tile alignment");
-static_assert(kRawBytes <= kXbufBytes && kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kOffRaw % 1024 == 0 && kOffFac % 16 == 0 && kOffMbar % 8 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 
 // ---- tensor memory columns
 constexpr uint32_t kColG = 0;      // G, then in place [M_0 | M_1] per 16 tokens (8 + 8 columns of bf16 pairs)
@@ -405,21 +404,19 @@ constexpr uint32_t kColY = 128;    // Y, 64 columns per head
 constexpr uint32_t kColW = 256;    // (w o X)^T, A operand: 64 columns hi, 64 columns lo
 constexpr uint32_t kColS = 384;    // a chunk's (w o X)^T B [p' = lane][n], fp32
 
-// ---- warps: three groups of 8 and three single ones (a fourth is idle: the
+// ---- warps: groups of 8, 8 and 12 and single ones (one of 4 is idle: the
 // register shares below are given to whole sets of 4 warps)
-constexpr int kGroup = 256;
-constexpr int kProducerWarp = 24, kHelperWarp = 25, kPublisherWarp = 26;
-constexpr int kThreads = 28 * 32;
-// registers a thread: 896 threads are launched with 72; the Y group holds the
-// state (64 values a thread) and the X group its channel's raw tokens
-constexpr int kRegsLaunch = 72, kRegsM = 56, kRegsY = 96, kRegsX = 80, kRegsOne = 40;
-static_assert((kRegsM + kRegsY + kRegsX) * kGroup + kRegsOne * 128 <= kRegsLaunch * kThreads, "register shares");
+constexpr int kMGroup = 256, kYGroup = 256, kXGroup = 384;   // threads
+constexpr int kYWarp = 8, kXWarp = 16, kProducerWarp = 28, kHelperWarp = 29, kPublisherWarp = 30;
+constexpr int kThreads = 32 * 32;
+// registers a thread: 1024 threads are launched with 64; the Y group holds
+// the state (64 values a thread)
+constexpr int kRegsLaunch = 64, kRegsM = 64, kRegsY = 104, kRegsX = 48, kRegsOne = 32;
+static_assert(kRegsM * kMGroup + kRegsY * kYGroup + kRegsX * kXGroup + kRegsOne * 128 <= kRegsLaunch * kThreads, "register shares");
 
 template <int kRegs> __device__ __forceinline__ void take_registers()
 {
-    if constexpr (kRegs == kRegsLaunch)
-        return;
-    else if constexpr (kRegs > kRegsLaunch)
+    if constexpr (kRegs > kRegsLaunch)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -433,29 +430,33 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-__device__ __forceinline__ void grp_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+// Barriers over a group's threads (named barrier `id`).
+template <int kCount> __device__ __forceinline__ void grp_sync(int id)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCount) : "memory");
+}
 
-__device__ __forceinline__ bool grp_or(int id, bool pred)
+template <int kCount> __device__ __forceinline__ bool grp_or(int id, bool pred)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %2, 0;\n\t"
-        "bar.red.or.pred q, %1, 256, p;\n\t"
+        "bar.red.or.pred q, %1, %3, p;\n\t"
         "selp.b32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"(id), "r"((uint32_t)pred) : "memory");
+        : "=r"(r) : "r"(id), "r"((uint32_t)pred), "n"(kCount) : "memory");
     return r != 0;
 }
 
-__device__ __forceinline__ bool grp_and(int id, bool pred)
+template <int kCount> __device__ __forceinline__ bool grp_and(int id, bool pred)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %2, 0;\n\t"
-        "bar.red.and.pred q, %1, 256, p;\n\t"
+        "bar.red.and.pred q, %1, %3, p;\n\t"
         "selp.b32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"(id), "r"((uint32_t)pred) : "memory");
+        : "=r"(r) : "r"(id), "r"((uint32_t)pred), "n"(kCount) : "memory");
     return r != 0;
 }
 
@@ -469,14 +470,15 @@ __device__ __forceinline__ bool grp_and(int id, bool pred)
 //   warps 0..7   M group: M(k) in place over G(k).
 //   warps 8..15  Y group: the state (in registers) and its bf16 copy; the rows
 //                of C S^T scaled by exp(c_t) in place, ready for M X to be
-//                added; the finished rows to the chunk's x buffer.
-//   warps 16..23 X group: conv + SiLU of the chunk's raw rows; X^T in place in
-//                the x buffer, both halves of (w o X)^T to tensor memory.
-//                (lane = channel, so that a thread's tokens are consecutive:
-//                16-byte stores of X^T, and the A operand's layout.)
-//   warp 24      producer: every MMA, the B/C tile loads.
-//   warp 25      helper: dt copies, prefix sums and factors, two chunks ahead.
-//   warp 26      publisher: finished rows to y, then the x load of chunk k+2.
+//                added; the finished rows over the chunk's X^T.
+//   warps 16..27 X group: conv + SiLU of the chunk's raw rows; X^T to shared
+//                memory, both halves of (w o X)^T to tensor memory.  (lane =
+//                channel, so that a thread's tokens are consecutive: 16-byte
+//                stores of X^T, and the A operand's layout.)  The largest
+//                share of the instructions, so the largest group.
+//   warp 28      producer: every MMA, the B/C tile loads.
+//   warp 29      helper: dt copies, prefix sums and factors, two chunks ahead.
+//   warp 30      publisher: finished rows to y.
 template <bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_bc,
@@ -517,10 +519,11 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     int *any_bad = reinterpret_cast<int *>(sm + kOffAnyBad);
     const uint32_t mb = sbase + kOffMbar;
     const uint32_t mb_bc = mb;            // [k] B/C tiles landed (state-only: even chunks, odd ones at mb_g)
-    const uint32_t mb_x0 = mb + 8;        // raw x landed in buffer k % 2 (+8)
+    const uint32_t mb_x = mb + 8;         // [k] raw x landed
+    const uint32_t mb_cs = mb + 16;       // [k] the copy of the state entering it ready
     const uint32_t mb_g = mb + 24;        // [k] G done
     const uint32_t mb_m = mb + 32;        // [k] M ready
-    const uint32_t mb_s = mb + 40;        // [k] the copy of the state entering it ready, kColS read
+    const uint32_t mb_s = mb + 40;        // [k] kColS free (the last chunk's products taken)
     const uint32_t mb_yo = mb + 48;       // [k] C S^T done
     const uint32_t mb_ys = mb + 56;       // [k] its rows scaled
     const uint32_t mb_e = mb + 64;        // [k] M X done
@@ -531,6 +534,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const uint32_t mb_sd0 = mb + 96;      // state product done
     const uint32_t mb_dt0 = mb + 112;     // factors ready
     const uint32_t mb_free0 = mb + 128;   // their buffer free
+    const uint32_t mb_xf0 = mb + 144;     // X^T's buffer free (the rows over it stored)
     auto of = [](uint32_t pair, int k) { return pair + 8 * (k & 1); };
     auto phase = [](int k) -> uint32_t { return (k >> 1) & 1; };   // of a pair's barrier
     auto xbuf = [](int k) { return (k & 1) ? kOffX1 : kOffX0; };
@@ -539,30 +543,24 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     auto first_row = [&](int k) { return begin + (wk.chunk + k) * kQ; };
 
     auto issue_x = [&](int k) {
-        const uint32_t bar = mb_x0 + 8 * (k & 1);
-        tc::mbar_expect_tx(bar, kRawBytes);
-        tc::tma_load_3d(sbase + xbuf(k), &tm_x, hp * kPP, first_row(k) - 3, 0, bar);
+        tc::mbar_expect_tx(mb_x, kRawBytes);
+        tc::tma_load_3d(sbase + kOffRaw, &tm_x, hp * kPP, first_row(k) - 3, 0, mb_x);
     };
-    // B (hi and lo) and C tiles of chunk k: two arrivals of mb_bc's phase.
-    // The state-only walk has two B buffers (odd chunks in the C and S tiles).
+    // B hi, B lo and C tiles of chunk k: three arrivals of mb_bc's phase (two
+    // in the state-only walk, which has two B buffers: odd chunks in the C and
+    // X tiles, on mb_g).
     auto bh_off = [](int k) { return kStateOnly && (k & 1) ? kOffC : kOffBh; };
-    auto bl_off = [](int k) { return kStateOnly && (k & 1) ? kOffS : kOffBl; };
+    auto bl_off = [](int k) { return kStateOnly && (k & 1) ? kOffX0 : kOffBl; };
     auto b_bar = [&](int k) { return kStateOnly && (k & 1) ? mb_g : mb_bc; };
-    auto issue_b = [&](int k) {
+    auto issue_tile = [&](int k, uint32_t off, int col, uint32_t bar) {
         const int row = (wk.act + k) * kQ;
-        const uint32_t bar = b_bar(k);
-        tc::mbar_expect_tx(bar, 2 * kTile);
-        tc::tma_load_3d(sbase + bh_off(k), &tm_bc, 0, row, 0, bar);
-        tc::tma_load_3d(sbase + bh_off(k) + kTile / 2, &tm_bc, 64, row, 0, bar);
-        tc::tma_load_3d(sbase + bl_off(k), &tm_bc, 128, row, 0, bar);
-        tc::tma_load_3d(sbase + bl_off(k) + kTile / 2, &tm_bc, 192, row, 0, bar);
+        tc::mbar_expect_tx(bar, kTile);
+        tc::tma_load_3d(sbase + off, &tm_bc, col, row, 0, bar);
+        tc::tma_load_3d(sbase + off + kTile / 2, &tm_bc, col + 64, row, 0, bar);
     };
-    auto issue_c = [&](int k) {
-        const int row = (wk.act + k) * kQ;
-        tc::mbar_expect_tx(mb_bc, kTile);
-        tc::tma_load_3d(sbase + kOffC, &tm_bc, 256, row, 0, mb_bc);
-        tc::tma_load_3d(sbase + kOffC + kTile / 2, &tm_bc, 320, row, 0, mb_bc);
-    };
+    auto issue_bh = [&](int k) { issue_tile(k, bh_off(k), 0, b_bar(k)); };
+    auto issue_bl = [&](int k) { issue_tile(k, bl_off(k), kN, b_bar(k)); };
+    auto issue_c = [&](int k) { issue_tile(k, kOffC, 2 * kN, mb_bc); };
 
     // helper warp: dt of both heads (adjacent: one 4-byte copy per token)
     auto load_dt_async = [&](int k) {
@@ -587,22 +585,25 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         tc::prefetch_tmap(&tm_x);
         tc::prefetch_tmap(&tm_bc);
         if (!kStateOnly) tc::prefetch_tmap(&tm_y);
-        tc::mbar_init(mb_bc, kStateOnly ? 1 : 2);
-        tc::mbar_init(mb_x0, 1);
-        tc::mbar_init(mb_x0 + 8, 1);
-        for (uint32_t b = mb_g; b < mb_dt0; b += 8) tc::mbar_init(b, 1);
+        tc::mbar_init(mb_bc, kStateOnly ? 2 : 3);
+        tc::mbar_init(mb_g, kStateOnly ? 2 : 1);
+        for (uint32_t b = mb_x; b < mb_dt0; b += 8)
+            if (b != mb_g) tc::mbar_init(b, 1);
+        tc::mbar_init(mb_xf0, 1);
+        tc::mbar_init(mb_xf0 + 8, 1);
         tc::mbar_init(mb_dt0, 32);
         tc::mbar_init(mb_dt0 + 8, 32);
         tc::mbar_init(mb_free0, kStateOnly ? 2 : 3);
         tc::mbar_init(mb_free0 + 8, kStateOnly ? 2 : 3);
         if (nk > 0) {
             issue_x(0);
-            issue_b(0);
+            issue_bh(0);
+            issue_bl(0);
             if (!kStateOnly) issue_c(0);
         }
-        if (nk > 1) {
-            issue_x(1);
-            if (kStateOnly) issue_b(1);
+        if (kStateOnly && nk > 1) {
+            issue_bh(1);
+            issue_bl(1);
         }
     }
     if (warp == kHelperWarp) {
@@ -621,7 +622,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const bool issuer = elect_one();
         const uint64_t dC = tc::smem_desc(sbase + kOffC, 16, 1024);    // K-major A
         const uint64_t dBk = tc::smem_desc(sbase + kOffBh, 16, 1024);  // K-major B (G)
-        const uint64_t dS = tc::smem_desc(sbase + kOffS, 16, 1024);    // K-major B (C S^T)
+        const uint64_t dS = tc::smem_desc(sbase + kOffBl, 16, 1024);   // K-major B (C S^T)
         constexpr uint32_t idG = tc::idesc_bf16(128, 128, 0, 0);
         constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
         constexpr uint32_t idY = tc::idesc_bf16(128, 64, 0, 0);
@@ -674,10 +675,20 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (k + 2 < nk) {
                     wait(of(mb_sd0, k), phase(k));
                     if (!all_ok()) break;
-                    if (issuer) issue_b(k + 2);
+                    if (issuer) {
+                        issue_bh(k + 2);
+                        issue_bl(k + 2);
+                    }
                 }
             } else {
-                // Y = C S^T once the last chunk's rows are out of its columns
+                if (k + 1 < nk) {
+                    wait(of(mb_sd0, k), phase(k));
+                    if (!all_ok()) break;
+                    if (issuer) issue_bh(k + 1);
+                }
+                // Y = C S^T once the copy of S is in the B lo tile and the last
+                // chunk's rows are out of Y's columns
+                wait(mb_cs, par);
                 if (k > 0) wait(mb_st, (k - 1) & 1);
                 if (!all_ok()) break;
                 tc::fence_after_sync();
@@ -688,14 +699,13 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::mma_commit(mb_yo);
                 }
                 __syncwarp();
-                // the tiles of the next chunk as soon as their last reader is done
                 if (k + 1 < nk) {
-                    wait(of(mb_sd0, k), phase(k));
-                    if (!all_ok()) break;
-                    if (issuer) issue_b(k + 1);
                     wait(mb_yo, par);
                     if (!all_ok()) break;
-                    if (issuer) issue_c(k + 1);
+                    if (issuer) {
+                        issue_c(k + 1);
+                        issue_bl(k + 1);
+                    }
                 }
                 wait(mb_ys, par);
                 wait(mb_m, par);
@@ -811,10 +821,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         tc::tma_store_3d(&tm_y, st, hp * kPP, row, 0);
                         tc::tma_store_3d(&tm_y, st + kTile / 2, hp * kPP + kP, row, 0);
                         tc::bulk_commit();
-                        if (k + 2 < nk) {
-                            tc::bulk_wait_read0();   // the rows have been read
-                            issue_x(k + 2);
-                        }
+                        tc::bulk_wait_read0();   // the rows have been read
+                        tc::mbar_arrive(of(mb_xf0, k));
                     }
                 } else {
                     // the prompt's end (always its walk's last chunk): its rows
@@ -833,126 +841,135 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
             __syncwarp();
         }
-    } else if (warp < 8) {
-        // ================= M group: thread (t = row, h) builds, for both
-        // heads, its share of M's 16-slot units in row t (M in place over G:
-        // the 16 G columns of a unit become [M_0 | M_1], 8 columns of bf16
-        // pairs each, so no other thread reads them)
+    } else if (warp < kYWarp) {
+        // ================= M group, in place over G: the 16 G columns of unit
+        // U (tokens 16 U .. 16 U + 15) become [M_0 | M_1] (8 columns of bf16
+        // pairs each).  Thread: row t, both heads; the two warps h of a
+        // quarter's rows share its units: the `quad` units h quad ..
+        // h quad + quad - 1 below its diagonal block and unit 2 quad + h of
+        // that block (past it: zeros).
         take_registers<kRegsM>();
         if constexpr (!kStateOnly) {
-            const int h = tid >> 7, quad = warp & 3;
-            const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+            const int h = warp >> 2, quad = warp & 3, row = tid & 127;
+            const uint32_t gcol = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kColG;
             const float D0 = p.D[2 * hp], D1 = p.D[2 * hp + 1];
             auto a_wait = [&](uint32_t bar, uint32_t parity) -> bool {
                 bool w = true;
                 if (tid == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-                return grp_and(1, w);
+                return grp_and<kMGroup>(1, w);
             };
             bool ok = true;
             for (int k = 0; k < nk; ++k) {
                 const int par = k & 1;
-                ok = a_wait(mb_dt0 + 8 * par, phase(k));
+                ok = a_wait(of(mb_dt0, k), phase(k));
                 if (ok) ok = a_wait(mb_g, par);
                 if (!ok) break;
                 tc::fence_after_sync();
-                const int row = tc::no_hoist(tid & 127);
-                // units past the row's 32-slot block are zero (s > t); of the
-                // others, warp h takes the factorised units h*quad ..
-                // h*quad+quad-1 and the diagonal unit 2 quad + h
-                {
-                    uint32_t z[16];
+                const float *c0 = cum + 2 * par * kQ;   // this chunk's factors, head 0 (head 1: + kQ)
+                uint32_t g[16], next[16];
+                auto unit = [&](int i) { return i < quad ? h * quad + i : 2 * quad + h; };
+                tc::tmem_ld16_nw(gcol + 16 * unit(0), g);
+                tc::tmem_wait_ld16(g);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = 0u;
+                for (int i = 0; i < 16; ++i) next[i] = 0u;
 #pragma unroll 1
-                    for (int U = 2 * quad + 2 + h; U < 8; U += 2)
-                        tc::tmem_st16_nw(tmem + lane_base + kColG + 16 * U, z);
-                }
+                for (int U = 2 * quad + 2 + h; U < 8; U += 2) tc::tmem_st16_nw(gcol + 16 * U, next);
 #pragma unroll 1
-                for (int iu = 0; iu <= quad; ++iu) {
-                    const int U = iu < quad ? h * quad + iu : 2 * quad + h;
-                    const int jb = U >> 1, u = U & 1;   // 32-slot block of s, half of it
-                    const uint32_t col = tmem + lane_base + kColG + 16 * U;
-                    uint32_t gu[16];
-                    tc::tmem_ld16_nw(col, gu);
-                    tc::tmem_wait_ld16(gu);
-                    const int s0 = 16 * U;
+                for (int i = 0; i < quad; ++i) {
+                    // below the diagonal block: exp(c_t - c_R) exp(c_R - c_s), both <= 1
+                    const int U = h * quad + i;
+                    tc::tmem_ld16_nw(gcol + 16 * unit(i + 1), next);   // under this unit's arithmetic
 #pragma unroll
                     for (int hd = 0; hd < 2; ++hd) {
-                        const float *cm = cum + (par * 2 + hd) * kQ;
-                        const float ct = cm[row];
+                        const float *cm = c0 + hd * kQ;
+                        const float et = tc::exp2_approx(cm[row] - cm[16 * U | 31]);
+                        const float2 et2 = make_float2(et, et);
+                        const float4 *fb = reinterpret_cast<const float4 *>(cm + (kOffFB - kOffCum) / 4 + 16 * U);
                         uint32_t out[8];
-                        if (jb < quad) {
-                            // block below the diagonal: exp(c_t - c_R) exp(c_R - c_s), both <= 1
-                            const float2 *fbh = reinterpret_cast<const float2 *>(fB + (par * 2 + hd) * kQ + s0);
-                            const float et = tc::exp2_approx(ct - cm[32 * jb + 31]);
-                            const float2 et2 = make_float2(et, et);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 g2 = make_float2(__uint_as_float(gu[2 * i]), __uint_as_float(gu[2 * i + 1]));
-                                const float2 m = tc::mul2(tc::mul2(g2, et2), fbh[i]);
-                                out[i] = tc::pack_bf16x2(m.x, m.y);
-                            }
-                        } else {
-                            const int r = (row & 31) - 16 * u;   // t's place in the unit
-                            const float Dh = hd ? D1 : D0;
-                            if (cm[32 * jb] - cm[32 * jb + 31] <= 60.0f) {   // warp-uniform
-                                // through 4-slot blocks: with the whole block's decay at
-                                // most 2^60 the row factor (>= 1 inside t's own) is finite
-                                const float *f4h = f4 + (par * 2 + hd) * kQ + s0;
-#pragma unroll
-                                for (int q4 = 0; q4 < 4; ++q4) {
-                                    const float rf = tc::exp2_approx(ct - cm[s0 + 4 * q4 + 3]);
-                                    float v[4];
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const int i = 4 * q4 + e;
-                                        const float x = fmaf(__uint_as_float(gu[i]) * rf, f4h[i], i == r ? Dh : 0.0f);
-                                        v[e] = i <= r ? x : 0.0f;
-                                    }
-                                    out[2 * q4] = tc::pack_bf16x2(v[0], v[1]);
-                                    out[2 * q4 + 1] = tc::pack_bf16x2(v[2], v[3]);
-                                }
-                            } else {
-                                // steep decays: one exponential per element, each <= 1
-                                const float *dh = dts + (par * 2 + hd) * kQ + s0;
-#pragma unroll
-                                for (int i2 = 0; i2 < 8; ++i2) {
-                                    float v[2];
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int i = 2 * i2 + e;
-                                        const float ex = tc::exp2_approx(fminf(ct - cm[s0 + i], 0.0f));
-                                        const float x = fmaf(__uint_as_float(gu[i]) * ex, dh[i], i == r ? Dh : 0.0f);
-                                        v[e] = i <= r ? x : 0.0f;
-                                    }
-                                    out[i2] = tc::pack_bf16x2(v[0], v[1]);
-                                }
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 f = fb[j];
+                            const float2 a = tc::mul2(tc::mul2(make_float2(__uint_as_float(g[4 * j]), __uint_as_float(g[4 * j + 1])), et2),
+                                                      make_float2(f.x, f.y));
+                            const float2 b = tc::mul2(tc::mul2(make_float2(__uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3])), et2),
+                                                      make_float2(f.z, f.w));
+                            out[2 * j] = tc::pack_bf16x2(a.x, a.y);
+                            out[2 * j + 1] = tc::pack_bf16x2(b.x, b.y);
                         }
-                        tc::tmem_st8_nw(col + 8 * hd, out);
+                        tc::tmem_st8_nw(gcol + 16 * U + 8 * hd, out);
                     }
+                    tc::tmem_wait_ld16(next);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) g[j] = next[j];
+                }
+                // the diagonal block's unit: column s = 16 h + i against row r of the block
+                const int r = (row & 31) - 16 * h;
+#pragma unroll 1
+                for (int hd = 0; hd < 2; ++hd) {
+                    const float *cb = c0 + hd * kQ + 32 * quad;   // the block's
+                    const float *cm = cb + 16 * h;                // the unit's
+                    const float ct = cb[row & 31], Dh = hd ? D1 : D0;
+                    uint32_t out[8];
+                    if (cb[0] - cb[31] <= 60.0f) {   // warp-uniform
+                        // through 4-token blocks: exp(c_t - c_R4) exp(c_R4 - c_s);
+                        // with the whole block's decay at most 2^60 the row
+                        // factor (>= 1 inside t's own) is finite
+                        const float4 *f4h = reinterpret_cast<const float4 *>(cm + (kOffF4 - kOffCum) / 4);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float rf = tc::exp2_approx(ct - cm[4 * j + 3]);
+                            const float4 f = f4h[j];
+                            const float fs[4] = {f.x, f.y, f.z, f.w};
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = 4 * j + e;
+                                const float x = fmaf(__uint_as_float(g[i]) * rf, fs[e], i == r ? Dh : 0.0f);
+                                v[e] = i <= r ? x : 0.0f;
+                            }
+                            out[2 * j] = tc::pack_bf16x2(v[0], v[1]);
+                            out[2 * j + 1] = tc::pack_bf16x2(v[2], v[3]);
+                        }
+                    } else {
+                        // steep decays (or a dt that is not finite): one
+                        // exponential per element, each <= 1
+                        const float *dh = cm + (kOffDt - kOffCum) / 4;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float v[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int i = 2 * j + e;
+                                const float ex = tc::exp2_approx(fminf(ct - cm[i], 0.0f));
+                                const float x = fmaf(__uint_as_float(g[i]) * ex, dh[i], i == r ? Dh : 0.0f);
+                                v[e] = i <= r ? x : 0.0f;
+                            }
+                            out[j] = tc::pack_bf16x2(v[0], v[1]);
+                        }
+                    }
+                    tc::tmem_st8_nw(gcol + 16 * (2 * quad + h) + 8 * hd, out);
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
-                grp_sync(1);
+                grp_sync<kMGroup>(1);
                 if (tid == 0) {
                     tc::mbar_arrive(mb_m);
-                    tc::mbar_arrive(mb_free0 + 8 * par);
+                    tc::mbar_arrive(of(mb_free0, k));
                 }
             }
             if (!ok && tid == 0) record_error(p.status, kStatusTimeout);
         }
-    } else if (warp < 16) {
+    } else if (warp < kXWarp) {
         // ================= Y group.  State: thread (p' = row, half of n), its
         // 64 values in registers.  Rows: thread (t = row, head).
         take_registers<kRegsY>();
-        const int tb = tid - kGroup;
+        const int tb = tid - 32 * kYWarp;
         const int hf = tb >> 7, quad = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
         auto b_wait = [&](uint32_t bar, uint32_t parity) -> bool {
             bool w = true;
             if (tb == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-            return grp_and(2, w);
+            return grp_and<kYGroup>(2, w);
         };
         const int prow = tb & 127;
         // this thread's values of the pair's state, [head][p][n] in memory
@@ -1004,7 +1021,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 w.y = tc::pack_bf16x2(st[4 * pc + 1].x, st[4 * pc + 1].y);
                 w.z = tc::pack_bf16x2(st[4 * pc + 2].x, st[4 * pc + 2].y);
                 w.w = tc::pack_bf16x2(st[4 * pc + 3].x, st[4 * pc + 3].y);
-                *reinterpret_cast<uint4 *>(sm + kOffS + hf * (kTile / 2) + tc::sw128(prow, pc)) = w;
+                *reinterpret_cast<uint4 *>(sm + kOffBl + hf * (kTile / 2) + tc::sw128(prow, pc)) = w;
             }
         };
         const uint32_t ycol = tmem + lane_base + kColY + 64 * hf;
@@ -1037,10 +1054,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tmem_ld16_nw(ycol + 16 * q, r);
                 tc::tmem_wait_ld16(r);
                 if (bad) {
-                    const uint8_t *b = bad_at + (k & 1) * 256 + 64 * hf + 16 * q;
+                    const uint8_t *b = bad_at + (k & 1) * 3 * kPP + 64 * hf + 16 * q;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (row >= min(b[i], b[128 + i])) r[i] = 0x7fffffffu;
+                        if (row >= min(min(b[i], b[kPP + i]), b[2 * kPP + i])) r[i] = 0x7fffffffu;
                 }
 #pragma unroll
                 for (int pc = 0; pc < 2; ++pc) {
@@ -1054,52 +1071,46 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
         };
         bool ok = true;
-        for (int k = 0; k <= nk; ++k) {
+        if (tb == 0) tc::mbar_arrive(mb_s);   // chunk 0's products may start
+        for (int k = 0; k < nk; ++k) {
             const int par = k & 1;
-            if (k > 0) {
-                // (factors of chunk k - 1: waited for when its rows were scaled)
-                ok = b_wait(of(mb_sd0, k - 1), phase(k - 1));
-                if (!ok) break;
-                tc::fence_after_sync();
-                next_state(k - 1);
+            ok = b_wait(of(mb_dt0, k), phase(k));
+            if (ok) ok = b_wait(of(mb_sd0, k), phase(k));   // the products done: kColS, and the B lo tile is free
+            if (!ok) break;
+            tc::fence_after_sync();
+            if constexpr (!kStateOnly) {
+                copy_state();
+                tc::fence_proxy_async();   // the copy, for the tensor core
+                grp_sync<kYGroup>(2);
+                if (tb == 0) tc::mbar_arrive(mb_cs);
             }
-            if (k < nk) {
-                // (C S^T of the last chunk has read the copy: waited for too)
-                if constexpr (!kStateOnly) {
-                    copy_state();
-                    tc::fence_proxy_async();   // the copy, for the tensor core
-                }
-                tc::fence_before_sync();       // the reads of kColS before the next products
-                grp_sync(2);
-                if (tb == 0) {
-                    tc::mbar_arrive(mb_s);
-                    if (k > 0) tc::mbar_arrive(of(mb_free0, k - 1));
-                }
-                if (kStateOnly) ok = b_wait(of(mb_dt0, k), phase(k));
-                if (!ok) break;
+            next_state(k);
+            tc::fence_before_sync();   // the reads of kColS before the next products
+            grp_sync<kYGroup>(2);
+            if (tb == 0) {
+                tc::mbar_arrive(mb_s);
+                if (kStateOnly) tc::mbar_arrive(of(mb_free0, k));
             }
             if constexpr (!kStateOnly) {
-                if (k > 0) {
-                    ok = b_wait(mb_e, (k - 1) & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    stage_rows(k - 1);
-                    tc::fence_proxy_async();   // the rows, for the TMA store
-                    tc::fence_before_sync();   // TMEM reads before the next product writes
-                    grp_sync(2);
-                    if (tb == 0) tc::mbar_arrive(mb_st);
+                ok = b_wait(mb_yo, par);
+                if (!ok) break;
+                tc::fence_after_sync();
+                scale_rows(k);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                grp_sync<kYGroup>(2);
+                if (tb == 0) {
+                    tc::mbar_arrive(mb_ys);
+                    tc::mbar_arrive(of(mb_free0, k));
                 }
-                if (k < nk) {
-                    ok = b_wait(of(mb_dt0, k), phase(k));
-                    if (ok) ok = b_wait(mb_yo, par);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    scale_rows(k);
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    grp_sync(2);
-                    if (tb == 0) tc::mbar_arrive(mb_ys);
-                }
+                ok = b_wait(mb_e, par);
+                if (!ok) break;
+                tc::fence_after_sync();
+                stage_rows(k);
+                tc::fence_proxy_async();   // the rows, for the TMA store
+                tc::fence_before_sync();   // TMEM reads before the next product writes
+                grp_sync<kYGroup>(2);
+                if (tb == 0) tc::mbar_arrive(mb_st);
             }
         }
         if (ok && (kStateOnly || wk.last) && (nk > 0 || !resume)) {
@@ -1116,87 +1127,83 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (!ok && tb == 0) record_error(p.status, kStatusTimeout);
     } else if (warp < kProducerWarp) {
         // ================= X group: thread (channel p' = lane of its quarter,
-        // half of the tokens)
+        // a third of the tokens)
         take_registers<kRegsX>();
-        const int tx = tid - 2 * kGroup;
-        const int hf = tx >> 7, quad = warp & 3;
+        const int tx = tid - 32 * kXWarp;
+        const int third = tx >> 7, quad = warp & 3;
         const int pr = tx & 127;
         const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
         const int head = quad >> 1;
         auto c_wait = [&](uint32_t bar, uint32_t parity) -> bool {
             bool w = true;
             if (tx == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-            return grp_and(3, w);
+            return grp_and<kXGroup>(3, w);
         };
+        // this thread's tokens: 48, 40 and 40, in units of 8
+        const int u0 = third == 0 ? 0 : third == 1 ? 6 : 11, u1 = third == 0 ? 6 : third == 1 ? 11 : 16;
         const int c = hp * kPP + pr;
         const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)c * 4);
         const float bias = p.conv_b ? p.conv_b[c] : 0.0f;
         bool ok = true;
         for (int k = 0; k < nk; ++k) {
             const int par = k & 1, cnt = tokens(k);
-            uint32_t r[34];   // tokens 64 hf - 3 .. 64 hf + 63 of the chunk, in pairs (the last half unused)
-            ok = c_wait(mb_x0 + 8 * par, phase(k));
-            if (!ok) break;
-            {
-                const uint8_t *raw = sm + xbuf(k) + 64 * hf * (kPP * 2) + 2 * pr;
-                auto ld = [&](int i) -> uint32_t { return *reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2)); };
-#pragma unroll
-                for (int i = 0; i < 33; ++i) r[i] = ld(2 * i) | (ld(2 * i + 1) << 16);
-                r[33] = ld(66);
-            }
-            if (cnt < kQ) {
-                // tokens past the prompt's end are a neighbour's: zeros (what
-                // the conv makes of them meets dt = 0 and M = 0)
-                const int left = cnt - 64 * hf + 3;   // values of r that are this prompt's
-#pragma unroll
-                for (int i = 0; i < 34; ++i) {
-                    if (2 * i >= left) r[i] = 0u;
-                    else if (2 * i + 1 >= left) r[i] &= 0xffffu;
-                }
-            }
-            if (hf == 0 && k == 0 && wk.chunk == 0) {
-                // the 3 tokens before the prompt: its entry's tail, or zeros
-                const uint16_t *t16 = reinterpret_cast<const uint16_t *>(tail) + c;
-                const uint32_t a = resume ? t16[ch] : 0u, b = resume ? t16[2 * ch] : 0u, d = resume ? t16[3 * ch] : 0u;
-                r[0] = a | (b << 16);
-                r[1] = (r[1] & 0xffff0000u) | d;
-            }
-            // X^T replaces the raw rows once every thread has read them, and
-            // (w o X)^T the last chunk's once its product is done
-            ok = c_wait(of(mb_dt0, k), phase(k));
+            // X^T's buffer is free once the rows of the chunk before last are
+            // stored, (w o X)^T's columns once the last chunk's product is done
+            ok = c_wait(mb_x, par);
+            if (ok) ok = c_wait(of(mb_dt0, k), phase(k));
             if (ok) {
                 if (kStateOnly) {
-                    if (tx == 0 && k + 2 < nk) issue_x(k + 2);   // (no X^T there)
                     if (k > 1) ok = c_wait(of(mb_sd0, k - 2), phase(k - 2));
-                } else if (k > 0) {
-                    ok = c_wait(of(mb_sd0, k - 1), phase(k - 1));
+                } else {
+                    if (k > 1) ok = c_wait(of(mb_xf0, k - 2), phase(k - 2));
+                    if (ok && k > 0) ok = c_wait(of(mb_sd0, k - 1), phase(k - 1));
                 }
             }
             if (!ok) break;
             tc::fence_after_sync();
-            const float *ws = wgt + (par * 2 + head) * kQ + 64 * hf;
-            const uint32_t wcol = tmem + lane_base + kColW - (kStateOnly && par ? kColW : 0u) + 32 * hf;
-            uint8_t *xt = sm + xbuf(k) + hf * (kTile / 2);
-            const float2 wa = make_float2(w4.x, w4.x), wb = make_float2(w4.y, w4.y), wc = make_float2(w4.z, w4.z),
-                         wd = make_float2(w4.w, w4.w), b2 = make_float2(bias, bias);
-            // packed pairs of consecutive tokens: even ones are a word of r,
-            // odd ones straddle two
-            auto odd = [&](int i) { return make_float2(__uint_as_float(r[i] & 0xffff0000u), __uint_as_float(r[i + 1] << 16)); };
+            const uint8_t *raw = sm + kOffRaw + 2 * pr;
+            // raw value of row i of the tile (token i - 3 of the chunk); rows
+            // past the prompt's end are a neighbour's: zeros (what the conv
+            // makes of them meets dt = 0 and M = 0)
+            const int rows = cnt + 3;
+            auto ld = [&](int i) -> float {
+                const uint32_t v = *reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2));
+                return i < rows ? __uint_as_float(v << 16) : 0.0f;
+            };
+            float v0 = ld(8 * u0), v1 = ld(8 * u0 + 1), v2 = ld(8 * u0 + 2);
+            if (third == 0 && k == 0 && wk.chunk == 0) {
+                // the 3 tokens before the prompt: its entry's tail, or zeros
+                const __nv_bfloat16 *t = tail + c;
+                v0 = resume ? __bfloat162float(t[ch]) : 0.0f;
+                v1 = resume ? __bfloat162float(t[2 * ch]) : 0.0f;
+                v2 = resume ? __bfloat162float(t[3 * ch]) : 0.0f;
+            }
+            const float *ws = wgt + (par * 2 + head) * kQ;
+            const uint32_t wcol = tmem + lane_base + kColW - (kStateOnly && par ? kColW : 0u);
+            uint8_t *xt = sm + xbuf(k);
+            const float2 wa = make_float2(w4.x, w4.x), wc = make_float2(w4.z, w4.z), b2 = make_float2(bias, bias);
+            // unit u's 16 bytes of X^T's row
+            auto piece = [&](int u) { return (u >> 3) * (kTile / 2) + tc::sw128(pr, u & 7); };
             __nv_bfloat162 check = __float2bfloat162_rn(0.0f);   // NaN once an activation is not finite
-            float2 e0 = unpack2(r[0]), o0 = odd(0);
+#pragma unroll 1
+            for (int u = u0; u < u1; ++u) {
+                float v[11];
+                v[0] = v0; v[1] = v1; v[2] = v2;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                uint32_t hi[4], lo[4], xp[4];
+                for (int i = 0; i < 8; ++i) v[3 + i] = ld(8 * u + 3 + i);
+                v0 = v[8]; v1 = v[9]; v2 = v[10];
                 const float4 w01 = *reinterpret_cast<const float4 *>(ws + 8 * u);
                 const float4 w23 = *reinterpret_cast<const float4 *>(ws + 8 * u + 4);
+                uint32_t hi[4], lo[4], xp[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int i = 4 * u + j;   // tokens 2 i, 2 i + 1
-                    const float2 e1 = unpack2(r[i + 1]), o1 = odd(i + 1 < 33 ? i + 1 : 32);
-                    float2 a = tc::fma2(wa, e0, b2);
-                    a = tc::fma2(wb, o0, a);
-                    a = tc::fma2(wc, e1, a);
-                    a = tc::fma2(wd, o1, a);
+                    // tokens 2 j, 2 j + 1 of the unit: taps 0 and 2 as packed pairs
+                    float2 a = tc::fma2(wa, make_float2(v[2 * j], v[2 * j + 1]), b2);
+                    a = tc::fma2(wc, make_float2(v[2 * j + 2], v[2 * j + 3]), a);
+                    a.x = fmaf(w4.y, v[2 * j + 1], a.x);
+                    a.y = fmaf(w4.y, v[2 * j + 2], a.y);
+                    a.x = fmaf(w4.w, v[2 * j + 3], a.x);
+                    a.y = fmaf(w4.w, v[2 * j + 4], a.y);
                     const float2 x = silu2(a);
                     if constexpr (!kStateOnly) {
                         xp[j] = tc::pack_bf16x2(x.x, x.y);
@@ -1206,11 +1213,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     const float2 w = j == 0 ? make_float2(w01.x, w01.y) : j == 1 ? make_float2(w01.z, w01.w)
                                    : j == 2 ? make_float2(w23.x, w23.y) : make_float2(w23.z, w23.w);
                     split2(tc::mul2(x, w), hi[j], lo[j]);
-                    e0 = e1;
-                    o0 = o1;
                 }
                 if constexpr (!kStateOnly)
-                    *reinterpret_cast<uint4 *>(xt + tc::sw128(pr, u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
+                    *reinterpret_cast<uint4 *>(xt + piece(u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
                 tmem_st4_nw(wcol + 4 * u, hi);
                 tmem_st4_nw(wcol + 64 + 4 * u, lo);
             }
@@ -1219,21 +1224,22 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 bad = !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
                 int at = kQ;
                 if (bad) {
-                    for (int i = 63; i >= 0; --i) {
-                        uint16_t *v = reinterpret_cast<uint16_t *>(xt + tc::sw128(pr, i >> 3)) + (i & 7);
+                    for (int i = 8 * u1 - 1; i >= 8 * u0; --i) {
+                        uint16_t *v = reinterpret_cast<uint16_t *>(xt + piece(i >> 3)) + (i & 7);
                         if ((*v & 0x7f80u) == 0x7f80u) {
                             *v = 0;
-                            at = 64 * hf + i;
+                            at = i;
                         }
                     }
                 }
-                bad_at[par * 256 + tx] = (uint8_t)at;
+                bad_at[par * 3 * kPP + tx] = (uint8_t)at;
             }
             tc::tmem_wait_st();
             if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
             tc::fence_before_sync();
-            bad = grp_or(3, bad);
+            bad = grp_or<kXGroup>(3, bad);
             if (tx == 0) {
+                if (k + 1 < nk) issue_x(k + 1);   // (every thread has read the raw rows)
                 any_bad[par] = bad;
                 tc::mbar_arrive(of(mb_w0, k));
                 tc::mbar_arrive(mb_free0 + 8 * par);
