@@ -383,14 +383,15 @@ constexpr uint32_t kOffRaw = kOffX1 + kTile;        // raw x [131][128]
 constexpr uint32_t kRawBytes = kRawRows * kPP * 2;
 constexpr uint32_t kOffFac = kOffRaw + kRawBytes;   // per-slot factors, f32 [2 parity][2 head][128] each:
 constexpr uint32_t kFac = 2 * 2 * kQ * 4;
+constexpr int kParts = 5;                           // of a chunk's units: 3 x 4 (X group), 2 x 2 (M group)
 constexpr uint32_t kOffCum = kOffFac;               //   prefix sums of dt A, log2 units
 constexpr uint32_t kOffDt = kOffCum + kFac;         //   dt
 constexpr uint32_t kOffFB = kOffDt + kFac;          //   exp(c_R - c_s) dt_s, R = end of s's 32-slot block
 constexpr uint32_t kOffF4 = kOffFB + kFac;          //   exp(c_R4 - c_s) dt_s, R4 = s | 3
 constexpr uint32_t kOffWgt = kOffF4 + kFac;         //   w_s
 constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]: see next_state
-constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][3][128]: first token of X not finite (128: none)
-constexpr uint32_t kOffAnyBad = kOffBad + 768;      // int [2 parity]
+constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][part][128]: first token of X not finite (128: none)
+constexpr uint32_t kOffAnyBad = kOffBad + 2 * kParts * kPP;   // int [2 parity][X, M group]
 constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
 constexpr uint32_t kOffMbar = kOffDtBuf + 2 * kQ * 4;
 constexpr uint32_t kOffTmem = kOffMbar + 160;
@@ -411,7 +412,7 @@ constexpr int kYWarp = 8, kXWarp = 16, kProducerWarp = 28, kHelperWarp = 29, kPu
 constexpr int kThreads = 32 * 32;
 // registers a thread: 1024 threads are launched with 64; the Y group holds
 // the state (64 values a thread)
-constexpr int kRegsLaunch = 64, kRegsM = 64, kRegsY = 104, kRegsX = 48, kRegsOne = 32;
+constexpr int kRegsLaunch = 64, kRegsM = 56, kRegsY = 96, kRegsX = 56, kRegsOne = 40;
 static_assert(kRegsM * kMGroup + kRegsY * kYGroup + kRegsX * kXGroup + kRegsOne * 128 <= kRegsLaunch * kThreads, "register shares");
 
 template <int kRegs> __device__ __forceinline__ void take_registers()
@@ -467,15 +468,14 @@ template <int kCount> __device__ __forceinline__ bool grp_and(int id, bool pred)
 //
 // Warp roles (hand-offs through mbarriers, every wait bounded; [k] = once
 // per chunk):
-//   warps 0..7   M group: M(k) in place over G(k).
+//   warps 0..7   M group: M(k) in place over G(k); a quarter of the X group's
+//                work on chunk k + 1.
 //   warps 8..15  Y group: the state (in registers) and its bf16 copy; the rows
 //                of C S^T scaled by exp(c_t) in place, ready for M X to be
 //                added; the finished rows over the chunk's X^T.
-//   warps 16..27 X group: conv + SiLU of the chunk's raw rows; X^T to shared
-//                memory, both halves of (w o X)^T to tensor memory.  (lane =
-//                channel, so that a thread's tokens are consecutive: 16-byte
-//                stores of X^T, and the A operand's layout.)  The largest
-//                share of the instructions, so the largest group.
+//   warps 16..27 X group: conv + SiLU of the chunk's raw rows, X^T and both
+//                halves of (w o X)^T (the largest share of the instructions,
+//                so the largest group).
 //   warp 28      producer: every MMA, the B/C tile loads.
 //   warp 29      helper: dt copies, prefix sums and factors, two chunks ahead.
 //   warp 30      publisher: finished rows to y.
@@ -588,13 +588,15 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         tc::mbar_init(mb_bc, kStateOnly ? 2 : 3);
         tc::mbar_init(mb_g, kStateOnly ? 2 : 1);
         for (uint32_t b = mb_x; b < mb_dt0; b += 8)
-            if (b != mb_g) tc::mbar_init(b, 1);
+            if (b != mb_g && b != mb_w0 && b != mb_w0 + 8) tc::mbar_init(b, 1);
+        tc::mbar_init(mb_w0, 2);       // the X and the M group
+        tc::mbar_init(mb_w0 + 8, 2);
         tc::mbar_init(mb_xf0, 1);
         tc::mbar_init(mb_xf0 + 8, 1);
         tc::mbar_init(mb_dt0, 32);
         tc::mbar_init(mb_dt0 + 8, 32);
-        tc::mbar_init(mb_free0, kStateOnly ? 2 : 3);
-        tc::mbar_init(mb_free0 + 8, kStateOnly ? 2 : 3);
+        tc::mbar_init(mb_free0, 3);
+        tc::mbar_init(mb_free0 + 8, 3);
         if (nk > 0) {
             issue_x(0);
             issue_bh(0);
@@ -615,6 +617,117 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     tc::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + kOffTmem);
 
+    // conv + SiLU of channel p' = pr, units ua .. ub - 1 (8 tokens each) of
+    // chunk k: X^T to shared memory, both halves of (w o X)^T to tensor
+    // memory (lane = channel, so that a thread's tokens are consecutive:
+    // 16-byte stores of X^T, and the A operand's layout).  Returns whether an
+    // activation was not finite (it enters X^T as zero; the first such token
+    // goes to bad_at).
+    auto conv_units = [&](int k, int pr, int ua, int ub, float4 w4, float bias, int part) -> bool {
+        const int par = k & 1;
+        const uint8_t *raw = sm + kOffRaw + 2 * pr;
+        auto ld = [&](int i) -> float {   // row i of the tile: token i - 3 of the chunk
+            return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2))) << 16);
+        };
+        const int rows = tokens(k) + 3;   // rows past these are a neighbour's
+        float v0 = ld(8 * ua), v1 = ld(8 * ua + 1), v2 = ld(8 * ua + 2);
+        if (ua == 0 && k == 0 && wk.chunk == 0) {
+            // the 3 tokens before the prompt: its entry's tail, or zeros
+            const __nv_bfloat16 *t = tail + hp * kPP + pr;
+            v0 = resume ? __bfloat162float(t[ch]) : 0.0f;
+            v1 = resume ? __bfloat162float(t[2 * ch]) : 0.0f;
+            v2 = resume ? __bfloat162float(t[3 * ch]) : 0.0f;
+        } else {
+            if (8 * ua >= rows) v0 = 0.0f;
+            if (8 * ua + 1 >= rows) v1 = 0.0f;
+            if (8 * ua + 2 >= rows) v2 = 0.0f;
+        }
+        const float *ws = wgt + (par * 2 + (pr >> 6)) * kQ;
+        const uint32_t wcol = tmem + (static_cast<uint32_t>(pr & 96) << 16) + kColW - (kStateOnly && par ? kColW : 0u);
+        uint8_t *xt = sm + xbuf(k);
+        const float2 wa = make_float2(w4.x, w4.x), wc = make_float2(w4.z, w4.z), b2 = make_float2(bias, bias);
+        // unit u's 16 bytes of X^T's row
+        auto piece = [&](int u) { return (u >> 3) * (kTile / 2) + tc::sw128(pr, u & 7); };
+        __nv_bfloat162 check = __float2bfloat162_rn(0.0f);   // NaN once an activation is not finite
+#pragma unroll 1
+        for (int u = ua; u < ub; ++u) {
+            float v[11];
+            v[0] = v0; v[1] = v1; v[2] = v2;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[3 + i] = ld(8 * u + 3 + i);
+            if (8 * u + 11 > rows) {
+                // a neighbour's rows: zeros (what the conv makes of them meets
+                // dt = 0 and M = 0)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (8 * u + 3 + i >= rows) v[3 + i] = 0.0f;
+            }
+            v0 = v[8]; v1 = v[9]; v2 = v[10];
+            const float4 w01 = *reinterpret_cast<const float4 *>(ws + 8 * u);
+            const float4 w23 = *reinterpret_cast<const float4 *>(ws + 8 * u + 4);
+            uint32_t hi[4], lo[4], xp[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // tokens 2 j, 2 j + 1 of the unit: taps 0 and 2 as packed pairs
+                float2 a = tc::fma2(wa, make_float2(v[2 * j], v[2 * j + 1]), b2);
+                a = tc::fma2(wc, make_float2(v[2 * j + 2], v[2 * j + 3]), a);
+                a.x = fmaf(w4.y, v[2 * j + 1], a.x);
+                a.y = fmaf(w4.y, v[2 * j + 2], a.y);
+                a.x = fmaf(w4.w, v[2 * j + 3], a.x);
+                a.y = fmaf(w4.w, v[2 * j + 4], a.y);
+                const float2 x = silu2(a);
+                if constexpr (!kStateOnly) {
+                    xp[j] = tc::pack_bf16x2(x.x, x.y);
+                    check = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&xp[j]), __float2bfloat162_rn(0.0f),
+                                    check);
+                }
+                const float2 w = j == 0 ? make_float2(w01.x, w01.y) : j == 1 ? make_float2(w01.z, w01.w)
+                               : j == 2 ? make_float2(w23.x, w23.y) : make_float2(w23.z, w23.w);
+                split2(tc::mul2(x, w), hi[j], lo[j]);
+            }
+            if constexpr (!kStateOnly)
+                *reinterpret_cast<uint4 *>(xt + piece(u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
+            tmem_st4_nw(wcol + 4 * u, hi);
+            tmem_st4_nw(wcol + 64 + 4 * u, lo);
+        }
+        bool bad = false;
+        if constexpr (!kStateOnly) {
+            bad = !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
+            int at = kQ;
+            if (bad) {
+                for (int i = 8 * ub - 1; i >= 8 * ua; --i) {
+                    uint16_t *v = reinterpret_cast<uint16_t *>(xt + piece(i >> 3)) + (i & 7);
+                    if ((*v & 0x7f80u) == 0x7f80u) {
+                        *v = 0;
+                        at = i;
+                    }
+                }
+            }
+            bad_at[(par * kParts + part) * kPP + pr] = (uint8_t)at;
+        }
+        tc::tmem_wait_st();
+        if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
+        tc::fence_before_sync();
+        return bad;
+    };
+    // One thread's waits (after one that gave up, the rest are not tried).
+    auto wait = [&](bool ok, uint32_t bar, uint32_t parity) -> bool {
+        return ok && tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+    };
+    // What conv_units(k) waits for: the raw rows, the factors, X^T's buffer
+    // (the rows of the chunk before last stored) and (w o X)^T's columns (the
+    // last chunk's product done; the state-only walk has two sets of them).
+    auto x_ready = [&](int k) -> bool {
+        bool ok = wait(true, of(mb_dt0, k), phase(k));
+        if (kStateOnly) {
+            if (k > 1) ok = wait(ok, of(mb_sd0, k - 2), phase(k - 2));
+        } else {
+            if (k > 1) ok = wait(ok, of(mb_xf0, k - 2), phase(k - 2));
+            if (k > 0) ok = wait(ok, of(mb_sd0, k - 1), phase(k - 1));
+        }
+        return wait(ok, mb_x, k & 1);
+    };
+
     if (warp >= kProducerWarp) take_registers<kRegsOne>();
     if (warp == kProducerWarp) {
         // the whole warp follows the loop, one elected lane issues: what the
@@ -627,10 +740,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
         constexpr uint32_t idY = tc::idesc_bf16(128, 64, 0, 0);
         bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            if (ok) ok = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-            return ok;
-        };
+        auto take = [&](uint32_t bar, uint32_t parity) { ok = wait(ok, bar, parity); };
         // a wait that gave up in one lane gives up in all
         auto all_ok = [&]() { return ok = __all_sync(0xffffffffu, ok); };
         auto koff = [](int ks) -> uint32_t { return (ks >> 2) * (kTile / 2) + (ks & 3) * 32; };   // K-major step
@@ -644,7 +754,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             __syncwarp();
         };
         if (!kStateOnly && nk > 0) {
-            wait(mb_bc, 0);
+            take(mb_bc, 0);
             if (all_ok()) {
                 tc::fence_after_sync();
                 issue_g();
@@ -653,10 +763,11 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         for (int k = 0; k < nk && ok; ++k) {
             const uint32_t par = k & 1;
             // (w o X)^T B: hi hi, lo hi, hi lo
-            if (kStateOnly) wait(b_bar(k), phase(k));
-            wait(mb_s, par);
-            wait(of(mb_w0, k), phase(k));
+            if (kStateOnly) take(b_bar(k), phase(k));
+            take(mb_s, par);
+            take(of(mb_w0, k), phase(k));
             if (!all_ok()) break;
+            if (issuer && k + 1 < nk) issue_x(k + 1);   // (the raw rows have been read)
             tc::fence_after_sync();
             if (issuer) {
                 const uint64_t dBh = tc::smem_desc(sbase + bh_off(k), kTile / 2, 1024);   // MN-major B
@@ -673,7 +784,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             __syncwarp();
             if constexpr (kStateOnly) {
                 if (k + 2 < nk) {
-                    wait(of(mb_sd0, k), phase(k));
+                    take(of(mb_sd0, k), phase(k));
                     if (!all_ok()) break;
                     if (issuer) {
                         issue_bh(k + 2);
@@ -682,14 +793,14 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
             } else {
                 if (k + 1 < nk) {
-                    wait(of(mb_sd0, k), phase(k));
+                    take(of(mb_sd0, k), phase(k));
                     if (!all_ok()) break;
                     if (issuer) issue_bh(k + 1);
                 }
                 // Y = C S^T once the copy of S is in the B lo tile and the last
                 // chunk's rows are out of Y's columns
-                wait(mb_cs, par);
-                if (k > 0) wait(mb_st, (k - 1) & 1);
+                take(mb_cs, par);
+                if (k > 0) take(mb_st, (k - 1) & 1);
                 if (!all_ok()) break;
                 tc::fence_after_sync();
                 if (issuer) {
@@ -700,15 +811,15 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
                 __syncwarp();
                 if (k + 1 < nk) {
-                    wait(mb_yo, par);
+                    take(mb_yo, par);
                     if (!all_ok()) break;
                     if (issuer) {
                         issue_c(k + 1);
                         issue_bl(k + 1);
                     }
                 }
-                wait(mb_ys, par);
-                wait(mb_m, par);
+                take(mb_ys, par);
+                take(mb_m, par);
                 if (!all_ok()) break;
                 tc::fence_after_sync();
                 // Y_h += M_h X_h
@@ -724,8 +835,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
                 __syncwarp();
                 if (k + 1 < nk) {
-                    wait(mb_e, par);
-                    wait(mb_bc, (k + 1) & 1);
+                    take(mb_e, par);
+                    take(mb_bc, (k + 1) & 1);
                     if (!all_ok()) break;
                     tc::fence_after_sync();
                     issue_g();
@@ -848,21 +959,19 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // quarter's rows share its units: the `quad` units h quad ..
         // h quad + quad - 1 below its diagonal block and unit 2 quad + h of
         // that block (past it: zeros).
+        // Between two Ms, while G is made: its share of the next chunk's conv.
         take_registers<kRegsM>();
-        if constexpr (!kStateOnly) {
+        {
             const int h = warp >> 2, quad = warp & 3, row = tid & 127;
             const uint32_t gcol = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kColG;
             const float D0 = p.D[2 * hp], D1 = p.D[2 * hp + 1];
-            auto a_wait = [&](uint32_t bar, uint32_t parity) -> bool {
-                bool w = true;
-                if (tid == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-                return grp_and<kMGroup>(1, w);
-            };
+            const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + row) * 4);
+            const float bias = p.conv_b ? p.conv_b[hp * kPP + row] : 0.0f;
             bool ok = true;
-            for (int k = 0; k < nk; ++k) {
+            for (int k = -1; k < nk; ++k) {
+              if (!kStateOnly && k >= 0) {
                 const int par = k & 1;
-                ok = a_wait(of(mb_dt0, k), phase(k));
-                if (ok) ok = a_wait(mb_g, par);
+                ok = grp_and<kMGroup>(1, tid != 0 || wait(true, mb_g, par));
                 if (!ok) break;
                 tc::fence_after_sync();
                 const float *c0 = cum + 2 * par * kQ;   // this chunk's factors, head 0 (head 1: + kQ)
@@ -956,6 +1065,18 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::mbar_arrive(mb_m);
                     tc::mbar_arrive(of(mb_free0, k));
                 }
+              }
+              if (k + 1 < nk) {
+                ok = grp_and<kMGroup>(1, tid != 0 || x_ready(k + 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const bool bad = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h, w4, bias, 3 + h));
+                if (tid == 0) {
+                    any_bad[2 * ((k + 1) & 1) + 1] = bad;
+                    tc::mbar_arrive(of(mb_w0, k + 1));
+                    if (kStateOnly) tc::mbar_arrive(of(mb_free0, k + 1));
+                }
+              }
             }
             if (!ok && tid == 0) record_error(p.status, kStatusTimeout);
         }
@@ -966,11 +1087,6 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int tb = tid - 32 * kYWarp;
         const int hf = tb >> 7, quad = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-        auto b_wait = [&](uint32_t bar, uint32_t parity) -> bool {
-            bool w = true;
-            if (tb == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-            return grp_and<kYGroup>(2, w);
-        };
         const int prow = tb & 127;
         // this thread's values of the pair's state, [head][p][n] in memory
         const size_t pair_off = (size_t)hp * kPP * kN + (size_t)prow * kN + 64 * hf;
@@ -1047,17 +1163,19 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         auto stage_rows = [&](int k) {
             const int row = tc::no_hoist(prow);
             uint8_t *box = sm + xbuf(k) + hf * (kTile / 2);
-            const bool bad = any_bad[k & 1] != 0;   // (rare: see the top)
+            const bool bad = any_bad[2 * (k & 1)] != 0 || any_bad[2 * (k & 1) + 1] != 0;   // (rare: see the top)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t r[16];
                 tc::tmem_ld16_nw(ycol + 16 * q, r);
                 tc::tmem_wait_ld16(r);
                 if (bad) {
-                    const uint8_t *b = bad_at + (k & 1) * 3 * kPP + 64 * hf + 16 * q;
+                    const uint8_t *b = bad_at + (k & 1) * kParts * kPP + 64 * hf + 16 * q;
+#pragma unroll 1
+                    for (int part = 0; part < kParts; ++part)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (row >= min(min(b[i], b[kPP + i]), b[2 * kPP + i])) r[i] = 0x7fffffffu;
+                        for (int i = 0; i < 16; ++i)
+                            if (row >= b[part * kPP + i]) r[i] = 0x7fffffffu;
                 }
 #pragma unroll
                 for (int pc = 0; pc < 2; ++pc) {
@@ -1074,8 +1192,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (tb == 0) tc::mbar_arrive(mb_s);   // chunk 0's products may start
         for (int k = 0; k < nk; ++k) {
             const int par = k & 1;
-            ok = b_wait(of(mb_dt0, k), phase(k));
-            if (ok) ok = b_wait(of(mb_sd0, k), phase(k));   // the products done: kColS, and the B lo tile is free
+            // the products done: kColS, and the B lo tile is free
+            ok = grp_and<kYGroup>(2, tb != 0 || wait(wait(true, of(mb_dt0, k), phase(k)), of(mb_sd0, k), phase(k)));
             if (!ok) break;
             tc::fence_after_sync();
             if constexpr (!kStateOnly) {
@@ -1092,7 +1210,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (kStateOnly) tc::mbar_arrive(of(mb_free0, k));
             }
             if constexpr (!kStateOnly) {
-                ok = b_wait(mb_yo, par);
+                ok = grp_and<kYGroup>(2, tb != 0 || wait(true, mb_yo, par));
                 if (!ok) break;
                 tc::fence_after_sync();
                 scale_rows(k);
@@ -1103,7 +1221,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::mbar_arrive(mb_ys);
                     tc::mbar_arrive(of(mb_free0, k));
                 }
-                ok = b_wait(mb_e, par);
+                ok = grp_and<kYGroup>(2, tb != 0 || wait(true, mb_e, par));
                 if (!ok) break;
                 tc::fence_after_sync();
                 stage_rows(k);
@@ -1130,119 +1248,19 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // a third of the tokens)
         take_registers<kRegsX>();
         const int tx = tid - 32 * kXWarp;
-        const int third = tx >> 7, quad = warp & 3;
-        const int pr = tx & 127;
-        const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-        const int head = quad >> 1;
-        auto c_wait = [&](uint32_t bar, uint32_t parity) -> bool {
-            bool w = true;
-            if (tx == 0) w = tc::mbar_wait_bounded(bar, parity, kWaitCycles);
-            return grp_and<kXGroup>(3, w);
-        };
-        // this thread's tokens: 48, 40 and 40, in units of 8
-        const int u0 = third == 0 ? 0 : third == 1 ? 6 : 11, u1 = third == 0 ? 6 : third == 1 ? 11 : 16;
-        const int c = hp * kPP + pr;
-        const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)c * 4);
-        const float bias = p.conv_b ? p.conv_b[c] : 0.0f;
+        const int third = tx >> 7, pr = tx & 127;   // units 4 third .. 4 third + 3
+        const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + pr) * 4);
+        const float bias = p.conv_b ? p.conv_b[hp * kPP + pr] : 0.0f;
         bool ok = true;
         for (int k = 0; k < nk; ++k) {
-            const int par = k & 1, cnt = tokens(k);
-            // X^T's buffer is free once the rows of the chunk before last are
-            // stored, (w o X)^T's columns once the last chunk's product is done
-            ok = c_wait(mb_x, par);
-            if (ok) ok = c_wait(of(mb_dt0, k), phase(k));
-            if (ok) {
-                if (kStateOnly) {
-                    if (k > 1) ok = c_wait(of(mb_sd0, k - 2), phase(k - 2));
-                } else {
-                    if (k > 1) ok = c_wait(of(mb_xf0, k - 2), phase(k - 2));
-                    if (ok && k > 0) ok = c_wait(of(mb_sd0, k - 1), phase(k - 1));
-                }
-            }
+            ok = grp_and<kXGroup>(3, tx != 0 || x_ready(k));
             if (!ok) break;
             tc::fence_after_sync();
-            const uint8_t *raw = sm + kOffRaw + 2 * pr;
-            // raw value of row i of the tile (token i - 3 of the chunk); rows
-            // past the prompt's end are a neighbour's: zeros (what the conv
-            // makes of them meets dt = 0 and M = 0)
-            const int rows = cnt + 3;
-            auto ld = [&](int i) -> float {
-                const uint32_t v = *reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2));
-                return i < rows ? __uint_as_float(v << 16) : 0.0f;
-            };
-            float v0 = ld(8 * u0), v1 = ld(8 * u0 + 1), v2 = ld(8 * u0 + 2);
-            if (third == 0 && k == 0 && wk.chunk == 0) {
-                // the 3 tokens before the prompt: its entry's tail, or zeros
-                const __nv_bfloat16 *t = tail + c;
-                v0 = resume ? __bfloat162float(t[ch]) : 0.0f;
-                v1 = resume ? __bfloat162float(t[2 * ch]) : 0.0f;
-                v2 = resume ? __bfloat162float(t[3 * ch]) : 0.0f;
-            }
-            const float *ws = wgt + (par * 2 + head) * kQ;
-            const uint32_t wcol = tmem + lane_base + kColW - (kStateOnly && par ? kColW : 0u);
-            uint8_t *xt = sm + xbuf(k);
-            const float2 wa = make_float2(w4.x, w4.x), wc = make_float2(w4.z, w4.z), b2 = make_float2(bias, bias);
-            // unit u's 16 bytes of X^T's row
-            auto piece = [&](int u) { return (u >> 3) * (kTile / 2) + tc::sw128(pr, u & 7); };
-            __nv_bfloat162 check = __float2bfloat162_rn(0.0f);   // NaN once an activation is not finite
-#pragma unroll 1
-            for (int u = u0; u < u1; ++u) {
-                float v[11];
-                v[0] = v0; v[1] = v1; v[2] = v2;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[3 + i] = ld(8 * u + 3 + i);
-                v0 = v[8]; v1 = v[9]; v2 = v[10];
-                const float4 w01 = *reinterpret_cast<const float4 *>(ws + 8 * u);
-                const float4 w23 = *reinterpret_cast<const float4 *>(ws + 8 * u + 4);
-                uint32_t hi[4], lo[4], xp[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // tokens 2 j, 2 j + 1 of the unit: taps 0 and 2 as packed pairs
-                    float2 a = tc::fma2(wa, make_float2(v[2 * j], v[2 * j + 1]), b2);
-                    a = tc::fma2(wc, make_float2(v[2 * j + 2], v[2 * j + 3]), a);
-                    a.x = fmaf(w4.y, v[2 * j + 1], a.x);
-                    a.y = fmaf(w4.y, v[2 * j + 2], a.y);
-                    a.x = fmaf(w4.w, v[2 * j + 3], a.x);
-                    a.y = fmaf(w4.w, v[2 * j + 4], a.y);
-                    const float2 x = silu2(a);
-                    if constexpr (!kStateOnly) {
-                        xp[j] = tc::pack_bf16x2(x.x, x.y);
-                        check = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&xp[j]), __float2bfloat162_rn(0.0f),
-                                        check);
-                    }
-                    const float2 w = j == 0 ? make_float2(w01.x, w01.y) : j == 1 ? make_float2(w01.z, w01.w)
-                                   : j == 2 ? make_float2(w23.x, w23.y) : make_float2(w23.z, w23.w);
-                    split2(tc::mul2(x, w), hi[j], lo[j]);
-                }
-                if constexpr (!kStateOnly)
-                    *reinterpret_cast<uint4 *>(xt + piece(u)) = make_uint4(xp[0], xp[1], xp[2], xp[3]);
-                tmem_st4_nw(wcol + 4 * u, hi);
-                tmem_st4_nw(wcol + 64 + 4 * u, lo);
-            }
-            bool bad = false;
-            if constexpr (!kStateOnly) {
-                bad = !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
-                int at = kQ;
-                if (bad) {
-                    for (int i = 8 * u1 - 1; i >= 8 * u0; --i) {
-                        uint16_t *v = reinterpret_cast<uint16_t *>(xt + piece(i >> 3)) + (i & 7);
-                        if ((*v & 0x7f80u) == 0x7f80u) {
-                            *v = 0;
-                            at = i;
-                        }
-                    }
-                }
-                bad_at[par * 3 * kPP + tx] = (uint8_t)at;
-            }
-            tc::tmem_wait_st();
-            if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
-            tc::fence_before_sync();
-            bad = grp_or<kXGroup>(3, bad);
+            const bool bad = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4, w4, bias, third));
             if (tx == 0) {
-                if (k + 1 < nk) issue_x(k + 1);   // (every thread has read the raw rows)
-                any_bad[par] = bad;
+                any_bad[2 * (k & 1)] = bad;
                 tc::mbar_arrive(of(mb_w0, k));
-                tc::mbar_arrive(mb_free0 + 8 * par);
+                tc::mbar_arrive(of(mb_free0, k));
             }
         }
         if (!ok && tx == 0) record_error(p.status, kStatusTimeout);
