@@ -63,7 +63,6 @@ constexpr int kPP = 2 * kP;        // x channels of a head pair
 constexpr int kAct = 3 * kN;       // operand row: B hi | B lo | C
 constexpr int kRawRows = kQ + 3;   // raw x rows of a chunk with the conv halo
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr long long kWaitCycles = 4000000000LL;   // ~2 s: bound of every wait
 
 // One walk: `chunks` chunks of prompt `seq` from chunk `chunk`, whose operand
 // rows start at chunk `act` of the operand array.
@@ -393,7 +392,8 @@ constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]
 constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][part][128]: first token of X not finite (128: none)
 constexpr uint32_t kOffAnyBad = kOffBad + 2 * kParts * kPP;   // int [2 parity][X, M group]
 constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
-constexpr uint32_t kOffMbar = kOffDtBuf + 2 * kQ * 4;
+constexpr uint32_t kOffTaps = kOffDtBuf + 2 * kQ * 4;   // float4 [128] conv taps, float [128] biases, float [2] D
+constexpr uint32_t kOffMbar = kOffTaps + kPP * 20 + 8;
 constexpr uint32_t kOffTmem = kOffMbar + 160;
 
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
@@ -412,7 +412,7 @@ constexpr int kYWarp = 8, kXWarp = 16, kProducerWarp = 28, kHelperWarp = 29, kPu
 constexpr int kThreads = 32 * 32;
 // registers a thread: 1024 threads are launched with 64; the Y group holds
 // the state (64 values a thread)
-constexpr int kRegsLaunch = 64, kRegsM = 56, kRegsY = 96, kRegsX = 56, kRegsOne = 40;
+constexpr int kRegsLaunch = 64, kRegsM = 64, kRegsY = 96, kRegsX = 48, kRegsOne = 48;
 static_assert(kRegsM * kMGroup + kRegsY * kYGroup + kRegsX * kXGroup + kRegsOne * 128 <= kRegsLaunch * kThreads, "register shares");
 
 template <int kRegs> __device__ __forceinline__ void take_registers()
@@ -421,6 +421,29 @@ template <int kRegs> __device__ __forceinline__ void take_registers()
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Bounded wait for phase `parity` of `bar`: false after kWaitTries tries (two
+// seconds and more).  Three instructions a try: the waiting threads of a walk
+// poll beside the warps that compute.
+constexpr uint32_t kWaitTries = 1u << 26;
+
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\t"
+        "mov.b32 n, %3;\n\t"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra TRY;\n\t"
+        "DONE:\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "n"(kWaitTries) : "memory");
+    return ok != 0;
 }
 
 // One lane of a converged warp.
@@ -485,8 +508,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                    const __grid_constant__ CUtensorMap tm_y, const PromptParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+    // (an offset, not a cast of the rounded address: so the compiler still
+    // knows the space, and addresses are 32 bits)
+    uint8_t *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = tc::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = p.H, ch = p.ch, HP = H / 2;
@@ -580,6 +604,13 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     };
 
     // ---- set-up
+    float4 *taps = reinterpret_cast<float4 *>(sm + kOffTaps);
+    float *biases = reinterpret_cast<float *>(sm + kOffTaps + kPP * 16);   // then D of both heads
+    if (tid < kPP) {
+        taps[tid] = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + tid) * 4);
+        biases[tid] = p.conv_b ? p.conv_b[hp * kPP + tid] : 0.0f;
+    }
+    if (tid < 2) biases[kPP + tid] = p.D[2 * hp + tid];
     if (warp == 0) tc::tmem_alloc(sbase + kOffTmem, 512);
     if (tid == 32 * kProducerWarp) {
         tc::prefetch_tmap(&tm_x);
@@ -623,8 +654,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // 16-byte stores of X^T, and the A operand's layout).  Returns whether an
     // activation was not finite (it enters X^T as zero; the first such token
     // goes to bad_at).
-    auto conv_units = [&](int k, int pr, int ua, int ub, float4 w4, float bias, int part) -> bool {
+    auto conv_units = [&](int k, int pr, int ua, int ub, int part) -> bool {
         const int par = k & 1;
+        const float4 w4 = taps[pr];
+        const float bias = biases[pr];
         const uint8_t *raw = sm + kOffRaw + 2 * pr;
         auto ld = [&](int i) -> float {   // row i of the tile: token i - 3 of the chunk
             return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2))) << 16);
@@ -649,7 +682,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // unit u's 16 bytes of X^T's row
         auto piece = [&](int u) { return (u >> 3) * (kTile / 2) + tc::sw128(pr, u & 7); };
         __nv_bfloat162 check = __float2bfloat162_rn(0.0f);   // NaN once an activation is not finite
-#pragma unroll 1
+#pragma unroll 2
         for (int u = ua; u < ub; ++u) {
             float v[11];
             v[0] = v0; v[1] = v1; v[2] = v2;
@@ -712,7 +745,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     };
     // One thread's waits (after one that gave up, the rest are not tried).
     auto wait = [&](bool ok, uint32_t bar, uint32_t parity) -> bool {
-        return ok && tc::mbar_wait_bounded(bar, parity, kWaitCycles);
+        return ok && mbar_wait(bar, parity);
     };
     // What conv_units(k) waits for: the raw rows, the factors, X^T's buffer
     // (the rows of the chunk before last stored) and (w o X)^T's columns (the
@@ -851,28 +884,31 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         for (int k = 0; k < nk; ++k) {
             const int b = k & 1;
             if (k >= 2) {
-                if (lane == 0) ok = tc::mbar_wait_bounded(mb_free0 + 8 * b, ((k >> 1) - 1) & 1, kWaitCycles);
+                if (lane == 0) ok = mbar_wait(mb_free0 + 8 * b, ((k >> 1) - 1) & 1);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
             const __nv_bfloat162 *src = reinterpret_cast<const __nv_bfloat162 *>(sm + kOffDtBuf) + b * kQ + 4 * lane;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 // slots 4 lane .. 4 lane + 3: prefix sums c and, for w, suffix
                 // sums c_last - c (from the end, so that the factors that
-                // matter, near the end, come from short sums)
+                // matter, near the end, come from short sums; shifted between
+                // lanes, not subtracted: a lane's own may be large)
                 const float Aw = h ? A1 : A0;
-                float d[4], a[4];
+                const int e = (b * 2 + h) * kQ + 4 * lane;
+                float d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = __bfloat1622float2(src[i]);
                     d[i] = h ? f.y : f.x;
-                    a[i] = d[i] * Aw;
                 }
-                const float own = (a[0] + a[1]) + (a[2] + a[3]);
-                float pre = own, suf = own;
+                *reinterpret_cast<float4 *>(dts + e) = make_float4(d[0], d[1], d[2], d[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] *= Aw;
+                float pre = (d[0] + d[1]) + (d[2] + d[3]), suf = pre;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const float u = __shfl_up_sync(0xffffffffu, pre, o);
@@ -881,37 +917,28 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     if (lane + o < 32) suf += v;
                 }
                 const float all = __shfl_sync(0xffffffffu, suf, 0);
-                // (shifted, not subtracted: own may be large against the rest)
-                float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
-                if (lane == 0) before = 0.0f;
-                if (lane == 31) after = 0.0f;
-                float c[4], w[4];
-                c[0] = before + a[0];
-                c[1] = c[0] + a[1];
-                c[2] = c[1] + a[2];
-                c[3] = c[2] + a[3];
-                w[3] = after;
-                w[2] = w[3] + a[3];
-                w[1] = w[2] + a[2];
-                w[0] = w[1] + a[1];
-                const int e = (b * 2 + h) * kQ + 4 * lane;
-                *reinterpret_cast<float4 *>(dts + e) = make_float4(d[0], d[1], d[2], d[3]);
-                *reinterpret_cast<float4 *>(cum + e) = make_float4(c[0], c[1], c[2], c[3]);
+                pre = __shfl_up_sync(0xffffffffu, pre, 1);
+                suf = __shfl_down_sync(0xffffffffu, suf, 1);
+                if (lane == 0) pre = 0.0f;
+                if (lane == 31) suf = 0.0f;
                 *reinterpret_cast<float4 *>(wgt + e) =
-                    make_float4(tc::exp2_approx(w[0]) * d[0], tc::exp2_approx(w[1]) * d[1],
-                                tc::exp2_approx(w[2]) * d[2], tc::exp2_approx(w[3]) * d[3]);
-                if constexpr (!kStateOnly) {
-                    *reinterpret_cast<float4 *>(f4 + e) =
-                        make_float4(tc::exp2_approx(c[3] - c[0]) * d[0], tc::exp2_approx(c[3] - c[1]) * d[1],
-                                    tc::exp2_approx(c[3] - c[2]) * d[2], d[3]);
-                    const float end = __shfl_sync(0xffffffffu, c[3], lane | 7);
-                    *reinterpret_cast<float4 *>(fB + e) =
-                        make_float4(tc::exp2_approx(end - c[0]) * d[0], tc::exp2_approx(end - c[1]) * d[1],
-                                    tc::exp2_approx(end - c[2]) * d[2], tc::exp2_approx(end - c[3]) * d[3]);
-                }
+                    make_float4(((suf + d[3]) + d[2]) + d[1], (suf + d[3]) + d[2], suf + d[3], suf);
+                *reinterpret_cast<float4 *>(cum + e) =
+                    make_float4(pre + d[0], (pre + d[0]) + d[1], ((pre + d[0]) + d[1]) + d[2],
+                                (((pre + d[0]) + d[1]) + d[2]) + d[3]);
                 // exp(c_last) S as S f + (S or 0): f = exp - 1 for slow decays
                 if (lane == 0)
-                    scl[b * 2 + h] = all > -1.0f ? make_float2(expm1f(all * kLn2), all) : make_float2(exp2f(all), all);
+                    scl[b * 2 + h] = make_float2(all > -1.0f ? expm1f(all * kLn2) : exp2f(all), all);
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int e = b * 2 * kQ + lane; e < (b + 1) * 2 * kQ; e += 32) {   // [parity][head][slot]
+                const float c = cum[e], d = dts[e];
+                wgt[e] = tc::exp2_approx(wgt[e]) * d;
+                if constexpr (!kStateOnly) {
+                    fB[e] = tc::exp2_approx(cum[e | 31] - c) * d;
+                    f4[e] = tc::exp2_approx(cum[e | 3] - c) * d;
+                }
             }
             if (k + 2 < nk) load_dt_async(k + 2);
             tc::mbar_arrive(mb_dt0 + 8 * b);
@@ -922,7 +949,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if constexpr (!kStateOnly) {
             bool ok = true;
             for (int k = 0; k < nk; ++k) {
-                if (lane == 0) ok = tc::mbar_wait_bounded(mb_st, k & 1, kWaitCycles);
+                if (lane == 0) ok = mbar_wait(mb_st, k & 1);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 const int cnt = tokens(k), row = first_row(k);
@@ -964,9 +991,6 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         {
             const int h = warp >> 2, quad = warp & 3, row = tid & 127;
             const uint32_t gcol = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kColG;
-            const float D0 = p.D[2 * hp], D1 = p.D[2 * hp + 1];
-            const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + row) * 4);
-            const float bias = p.conv_b ? p.conv_b[hp * kPP + row] : 0.0f;
             bool ok = true;
             for (int k = -1; k < nk; ++k) {
               if (!kStateOnly && k >= 0) {
@@ -975,19 +999,17 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (!ok) break;
                 tc::fence_after_sync();
                 const float *c0 = cum + 2 * par * kQ;   // this chunk's factors, head 0 (head 1: + kQ)
-                uint32_t g[16], next[16];
-                auto unit = [&](int i) { return i < quad ? h * quad + i : 2 * quad + h; };
-                tc::tmem_ld16_nw(gcol + 16 * unit(0), g);
-                tc::tmem_wait_ld16(g);
+                uint32_t g[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) next[i] = 0u;
+                for (int i = 0; i < 16; ++i) g[i] = 0u;
 #pragma unroll 1
-                for (int U = 2 * quad + 2 + h; U < 8; U += 2) tc::tmem_st16_nw(gcol + 16 * U, next);
+                for (int U = 2 * quad + 2 + h; U < 8; U += 2) tc::tmem_st16_nw(gcol + 16 * U, g);
 #pragma unroll 1
                 for (int i = 0; i < quad; ++i) {
                     // below the diagonal block: exp(c_t - c_R) exp(c_R - c_s), both <= 1
                     const int U = h * quad + i;
-                    tc::tmem_ld16_nw(gcol + 16 * unit(i + 1), next);   // under this unit's arithmetic
+                    tc::tmem_ld16_nw(gcol + 16 * U, g);
+                    tc::tmem_wait_ld16(g);
 #pragma unroll
                     for (int hd = 0; hd < 2; ++hd) {
                         const float *cm = c0 + hd * kQ;
@@ -1007,17 +1029,16 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         }
                         tc::tmem_st8_nw(gcol + 16 * U + 8 * hd, out);
                     }
-                    tc::tmem_wait_ld16(next);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) g[j] = next[j];
                 }
+                tc::tmem_ld16_nw(gcol + 16 * (2 * quad + h), g);
+                tc::tmem_wait_ld16(g);
                 // the diagonal block's unit: column s = 16 h + i against row r of the block
                 const int r = (row & 31) - 16 * h;
 #pragma unroll 1
                 for (int hd = 0; hd < 2; ++hd) {
                     const float *cb = c0 + hd * kQ + 32 * quad;   // the block's
                     const float *cm = cb + 16 * h;                // the unit's
-                    const float ct = cb[row & 31], Dh = hd ? D1 : D0;
+                    const float ct = cb[row & 31], Dh = biases[kPP + hd];
                     uint32_t out[8];
                     if (cb[0] - cb[31] <= 60.0f) {   // warp-uniform
                         // through 4-token blocks: exp(c_t - c_R4) exp(c_R4 - c_s);
@@ -1070,7 +1091,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 ok = grp_and<kMGroup>(1, tid != 0 || x_ready(k + 1));
                 if (!ok) break;
                 tc::fence_after_sync();
-                const bool bad = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h, w4, bias, 3 + h));
+                const bool bad = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h, 3 + h));
                 if (tid == 0) {
                     any_bad[2 * ((k + 1) & 1) + 1] = bad;
                     tc::mbar_arrive(of(mb_w0, k + 1));
@@ -1249,14 +1270,12 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         take_registers<kRegsX>();
         const int tx = tid - 32 * kXWarp;
         const int third = tx >> 7, pr = tx & 127;   // units 4 third .. 4 third + 3
-        const float4 w4 = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + pr) * 4);
-        const float bias = p.conv_b ? p.conv_b[hp * kPP + pr] : 0.0f;
         bool ok = true;
         for (int k = 0; k < nk; ++k) {
             ok = grp_and<kXGroup>(3, tx != 0 || x_ready(k));
             if (!ok) break;
             tc::fence_after_sync();
-            const bool bad = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4, w4, bias, third));
+            const bool bad = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4, third));
             if (tx == 0) {
                 any_bad[2 * (k & 1)] = bad;
                 tc::mbar_arrive(of(mb_w0, k));
