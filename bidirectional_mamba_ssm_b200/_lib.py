@@ -385,67 +385,59 @@ def bimamba_out_proj(y, w_out, out, stream=None):
     return out
 
 
-class _Args:
-    """The tensors of one call: each has to be a dense CUDA tensor of the
-    given type and shape, on one device, which is made current for the call
-    (the kernels launch there, on that device's current stream unless one is
-    given)."""
-
-    def __init__(self, where: str, lead: torch.Tensor, stream):
-        self.where, self.dev, self._stream = where, lead.device, stream
-        if lead.device.type != "cuda":
-            self.bad(f"a CUDA tensor is wanted, got one on {lead.device}")
-
-    def bad(self, why: str):
-        raise BimambaError(BIMAMBA_ERR_INVALID, f"{self.where}: {why}")
-
-    def ptr(self, name: str, t, dtype, shape) -> int:
-        if t.dtype is not dtype or t.shape != shape or t.device != self.dev or not t.is_contiguous():
-            self.bad(f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on {self.dev} is wanted, got "
-                     f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-        return t.data_ptr()
-
-    def opt(self, name: str, t, dtype, shape):
-        return None if t is None else self.ptr(name, t, dtype, shape)
-
-    def workspace(self, t):
+def _call(where, fn, stream, lead, before, specs, after):
+    """fn(*before, pointers of specs, *after, stream).  A spec is (name,
+    tensor or None, dtype, shape), a dense CUDA tensor on lead's device; a
+    number stands for itself.  That device is made current
+    for the call: the kernels launch there, on its current stream unless one
+    is given."""
+    index = lead.get_device()
+    if index < 0:
+        raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: a CUDA tensor is wanted, got one on {lead.device}")
+    args = list(before)
+    for spec in specs:
+        if spec.__class__ is not tuple:
+            args.append(spec)
+            continue
+        name, t, dtype, shape = spec
         if t is None:
-            return None, 0
-        if t.device != self.dev or not t.is_contiguous():
-            self.bad(f"workspace: a dense tensor on {self.dev} is wanted")
-        return t.data_ptr(), t.numel() * t.element_size()
-
-    def call(self, fn, *args):
-        index = self.dev.index
-        here = torch.cuda.current_device()
-        if here == index:
-            st = fn(*args, self._raw_stream(index))
-        else:
-            with torch.cuda.device(index):
-                st = fn(*args, self._raw_stream(index))
-        if st != BIMAMBA_OK:
-            raise BimambaError(st, self.where)
-
-    def _raw_stream(self, index):
-        s = self._stream
-        if s is None:
-            return torch.cuda.current_stream(index).cuda_stream
-        return s if isinstance(s, int) else s.cuda_stream
+            args.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: {name}: a dense {dtype} tensor of shape {tuple(shape)} "
+                               f"on {lead.device} is wanted, got {t.dtype} {tuple(t.shape)} with strides "
+                               f"{t.stride()} on {t.device}")
+        args.append(t.data_ptr())
+    args.extend(after)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _stream(stream))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, where)
 
 
-def _causal_args(a, xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state):
+def _workspace(where, t, lead):
+    """(pointer, bytes) of a call's workspace."""
+    if t is None:
+        return None, 0
+    if t.device != lead.device or not t.is_contiguous():
+        raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: workspace: a dense tensor on {lead.device} is wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _causal_inputs(xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state):
     """The inputs that the prompt scan and the token step share."""
-    rows, f32, td = xbc.shape[0], torch.float32, xbc.dtype
-    ch = heads * headdim + 2 * d_state
-    return (a.ptr("xbc", xbc, td, (rows, ch)), a.ptr("dt", dt, td, (rows, heads)),
-            a.ptr("A", A, f32, (heads,)), a.ptr("D", D, f32, (heads,)),
-            a.ptr("conv_w", conv_w, f32, (ch, 4)), a.opt("conv_b", conv_b, f32, (ch,)))
+    rows, f32, td, ch = xbc.shape[0], torch.float32, xbc.dtype, heads * headdim + 2 * d_state
+    return (("xbc", xbc, td, (rows, ch)), ("dt", dt, td, (rows, heads)), ("A", A, f32, (heads,)),
+            ("D", D, f32, (heads,)), ("conv_w", conv_w, f32, (ch, 4)), ("conv_b", conv_b, f32, (ch,)))
 
 
-def _pool_args(a, state_pool, tail_pool, dtype, heads, headdim, d_state):
+def _causal_pool(state_pool, tail_pool, dtype, heads, headdim, d_state):
     pool = state_pool.shape[0]
-    return (a.ptr("state_pool", state_pool, torch.float32, (pool, heads, headdim, d_state)),
-            a.ptr("tail_pool", tail_pool, dtype, (pool, 4, heads * headdim + 2 * d_state)), pool)
+    return (("state_pool", state_pool, torch.float32, (pool, heads, headdim, d_state)),
+            ("tail_pool", tail_pool, dtype, (pool, 4, heads * headdim + 2 * d_state)), pool)
 
 
 def bimamba_prompt_workspace_bytes(dims: Dims) -> int:
@@ -453,11 +445,11 @@ def bimamba_prompt_workspace_bytes(dims: Dims) -> int:
 
 
 def new_prompt_workspace(xbc, *, batch, heads, headdim, d_state) -> torch.Tensor:
-    """Zero-filled workspace for bimamba_prompt_scan on packed rows like
-    xbc's, for up to `batch` prompts."""
+    """Workspace for bimamba_prompt_scan on packed rows like xbc's, for up to
+    `batch` prompts."""
     n = bimamba_prompt_workspace_bytes(make_dims(batch, xbc.shape[0], heads, headdim, d_state,
                                                  _dtype_code(xbc)))
-    return torch.zeros(max(256, n), dtype=torch.uint8, device=xbc.device)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=xbc.device)
 
 
 def bimamba_prompt_scan(xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, tail_pool, slots,
@@ -467,16 +459,14 @@ def bimamba_prompt_scan(xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, t
     pool entry slots[s] gets the prompt's state and last raw tokens, and is
     what it continues from where resume[s] != 0 (resume None: nowhere).
     cu_seqlens, slots and resume are int32 device tensors."""
-    a = _Args("bimamba_prompt_scan", xbc, stream)
     td, n, i32 = xbc.dtype, slots.shape[0], torch.int32
     dims = make_dims(n, xbc.shape[0], heads, headdim, d_state, _dtype_code(xbc))
-    inputs = _causal_args(a, xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state)
-    pool = _pool_args(a, state_pool, tail_pool, td, heads, headdim, d_state)
-    ws, ws_bytes = a.workspace(workspace)
-    a.call(_lib.bimamba_prompt_scan, ctypes.byref(dims), *inputs,
-           a.ptr("cu_seqlens", cu_seqlens, i32, (n + 1,)), *pool, a.ptr("slots", slots, i32, (n,)),
-           a.opt("resume", resume, i32, (n,)), a.ptr("y", y, td, (xbc.shape[0], heads * headdim)), ws,
-           ws_bytes)
+    _call("bimamba_prompt_scan", _lib.bimamba_prompt_scan, stream, xbc, (ctypes.byref(dims),),
+          (*_causal_inputs(xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state),
+           ("cu_seqlens", cu_seqlens, i32, (n + 1,)),
+           *_causal_pool(state_pool, tail_pool, td, heads, headdim, d_state), ("slots", slots, i32, (n,)),
+           ("resume", resume, i32, (n,)), ("y", y, td, (xbc.shape[0], heads * headdim))),
+          _workspace("bimamba_prompt_scan", workspace, xbc))
     return y
 
 
@@ -495,15 +485,13 @@ def bimamba_token_step(xbc, dt, A, D, conv_w, conv_b, state_pool, tail_pool, slo
     """One new token of each of a batch of cached streams: row s of xbc
     (rows, ch) and dt (rows, H) continues from pool entry slots[s], which is
     updated in place, into row s of y (rows, H*P)."""
-    a = _Args("bimamba_token_step", xbc, stream)
     td, rows = xbc.dtype, xbc.shape[0]
     dims = make_dims(rows, 1, heads, headdim, d_state, _dtype_code(xbc))
-    inputs = _causal_args(a, xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state)
-    pool = _pool_args(a, state_pool, tail_pool, td, heads, headdim, d_state)
-    ws, ws_bytes = a.workspace(workspace)
-    a.call(_lib.bimamba_token_step, ctypes.byref(dims), *inputs, *pool,
-           a.ptr("slots", slots, torch.int32, (rows,)), a.ptr("y", y, td, (rows, heads * headdim)), ws,
-           ws_bytes)
+    _call("bimamba_token_step", _lib.bimamba_token_step, stream, xbc, (ctypes.byref(dims),),
+          (*_causal_inputs(xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state),
+           *_causal_pool(state_pool, tail_pool, td, heads, headdim, d_state),
+           ("slots", slots, torch.int32, (rows,)), ("y", y, td, (rows, heads * headdim))),
+          _workspace("bimamba_token_step", workspace, xbc))
     return y
 
 
@@ -512,15 +500,15 @@ def bimamba_layer_norm(x, gamma, beta, y, mean, rstd, *, residual=None, sum_out=
     """y = layer norm of x (+ residual) over the last dimension, gamma/beta
     (beta may be None) fp32; mean and rstd (one fp32 value a row) and, with a
     residual, sum_out = x + residual are written for the backward pass."""
-    a = _Args("bimamba_layer_norm", x, stream)
-    code, td, cols = _dtype_code(x), x.dtype, x.shape[-1]
+    td, shape, f32 = x.dtype, x.shape, torch.float32
+    cols, each = shape[-1], shape[:-1]
     rows = x.numel() // cols if cols else 0
-    f32, vec = torch.float32, (cols,)
-    a.call(_lib.bimamba_layer_norm, rows, cols, a.ptr("x", x, td, x.shape),
-           a.opt("residual", residual, td, x.shape), a.ptr("gamma", gamma, f32, vec),
-           a.opt("beta", beta, f32, vec), eps, a.ptr("y", y, td, x.shape),
-           a.opt("sum_out", sum_out, td, x.shape), a.ptr("mean", mean, f32, x.shape[:-1]),
-           a.ptr("rstd", rstd, f32, x.shape[:-1]), code)
+    vec = (cols,)
+    _call(
+        "bimamba_layer_norm", _lib.bimamba_layer_norm, stream, x, (rows, cols),
+        (("x", x, td, shape), ("residual", residual, td, shape), ("gamma", gamma, f32, vec),
+         ("beta", beta, f32, vec), eps, ("y", y, td, shape), ("sum_out", sum_out, td, shape),
+         ("mean", mean, f32, each), ("rstd", rstd, f32, each)), (_dtype_code(x),))
     return y
 
 
@@ -540,15 +528,15 @@ def bimamba_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dgamma, dbeta, wor
     """Gradients of the layer norm from dy (and dsum, the gradient that
     reaches h past the norm): writes dx, dgamma and, unless None, dbeta.
     h is the forward call's x, or its sum_out where it had a residual."""
-    a = _Args("bimamba_layer_norm_backward", h, stream)
-    code, td, cols = _dtype_code(h), h.dtype, h.shape[-1]
+    td, shape, f32 = h.dtype, h.shape, torch.float32
+    cols, each = shape[-1], shape[:-1]
     rows = h.numel() // cols if cols else 0
-    f32, vec, each = torch.float32, (cols,), h.shape[:-1]
-    ws, ws_bytes = a.workspace(workspace)
-    a.call(_lib.bimamba_layer_norm_backward, rows, cols, a.ptr("dy", dy, td, h.shape),
-           a.ptr("h", h, td, h.shape), a.ptr("gamma", gamma, f32, vec), a.ptr("mean", mean, f32, each),
-           a.ptr("rstd", rstd, f32, each), a.opt("dsum", dsum, td, h.shape), a.ptr("dx", dx, td, h.shape),
-           a.ptr("dgamma", dgamma, f32, vec), a.opt("dbeta", dbeta, f32, vec), code, ws, ws_bytes)
+    vec = (cols,)
+    _call("bimamba_layer_norm_backward", _lib.bimamba_layer_norm_backward, stream, h, (rows, cols),
+          (("dy", dy, td, shape), ("h", h, td, shape), ("gamma", gamma, f32, vec), ("mean", mean, f32, each),
+           ("rstd", rstd, f32, each), ("dsum", dsum, td, shape), ("dx", dx, td, shape),
+           ("dgamma", dgamma, f32, vec), ("dbeta", dbeta, f32, vec)),
+          (_dtype_code(h), *_workspace("bimamba_layer_norm_backward", workspace, h)))
     return dx
 
 

@@ -497,7 +497,9 @@ static int check_causal(const bimamba_dims *d, const void *xbc, const void *dt, 
 size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d)
 {
     if (check_dims(d) != BIMAMBA_OK) return 0;
-    return prompt_ticket_bytes(*d) + (prompt_tc_supported(*d) ? prompt_tc_ws_bytes(*d) : 0);
+    // (256 bytes at least: a workspace is always wanted)
+    const size_t n = prompt_tc_supported(*d) ? prompt_tc_ws_bytes(*d) : prompt_seq_ws_bytes(*d);
+    return (n + 511) & ~(size_t)255;
 }
 
 int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
@@ -519,8 +521,7 @@ int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, 
     q.cu_seqlens = cu_seqlens;
     q.state = state_pool; q.tail = tail_pool; q.pool = pool_size; q.slots = slots; q.resume = resume;
     q.y = y;
-    q.tickets = static_cast<int *>(workspace);
-    q.workspace = static_cast<char *>(workspace) + prompt_ticket_bytes(*d);
+    q.workspace = workspace;
     q.status = device_status_word();
     return cuda_status(launch_prompt(q, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -528,7 +529,7 @@ int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, 
 size_t bimamba_token_step_workspace_bytes(const bimamba_dims *d)
 {
     if (check_dims(d) != BIMAMBA_OK) return 0;
-    return prompt_ticket_bytes(*d);
+    return step_ticket_bytes(*d);
 }
 
 int bimamba_token_step(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
@@ -541,7 +542,7 @@ int bimamba_token_step(const bimamba_dims *d, const void *xbc, const void *dt, c
     if (d->len != 1) return BIMAMBA_ERR_INVALID;
     if (d->batch == 0) return BIMAMBA_OK;
     st = check_causal(d, xbc, dt, A, D, conv_w, conv_b, nullptr, state_pool, tail_pool, pool_size,
-                      slots, nullptr, y, workspace, workspace_bytes, prompt_ticket_bytes(*d));
+                      slots, nullptr, y, workspace, workspace_bytes, step_ticket_bytes(*d));
     if (st != BIMAMBA_OK) return st;
     StepProblem q{};
     q.rows = d->batch; q.H = d->heads; q.P = d->headdim; q.N = d->d_state; q.pool = pool_size;

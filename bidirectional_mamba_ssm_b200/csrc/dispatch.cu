@@ -23,7 +23,7 @@ cudaError_t launch_bimamba(const Problem &p, cudaStream_t stream)
     return launch_scan_seq<__nv_bfloat16>(p, stream);
 }
 
-size_t prompt_ticket_bytes(const bimamba_dims &d)
+size_t step_ticket_bytes(const bimamba_dims &d)
 {
     return ((size_t)d.batch * sizeof(int) + 255) & ~(size_t)255;
 }

@@ -138,15 +138,13 @@ struct PromptProblem {
     int pool;
     const int *slots, *resume;    // (batch); resume may be null
     void *y;
-    int *tickets;                 // (batch) zeros, returned to zero
     void *workspace;
     int *status;
 };
-// leading bytes of both operators' workspaces: the tickets
-size_t prompt_ticket_bytes(const bimamba_dims &d);
 cudaError_t launch_prompt(const PromptProblem &q, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_prompt_seq(const PromptProblem &q, cudaStream_t stream);
+size_t prompt_seq_ws_bytes(const bimamba_dims &d);
 bool prompt_tc_supported(const bimamba_dims &d);   // bf16, headdim 64, d_state 128, even heads
 size_t prompt_tc_ws_bytes(const bimamba_dims &d);
 cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream);
@@ -163,6 +161,7 @@ struct StepProblem {
     int *tickets;                 // (rows) zeros, returned to zero
     int *status;
 };
+size_t step_ticket_bytes(const bimamba_dims &d);   // the workspace: the tickets
 template <typename T>
 cudaError_t launch_token_step(const StepProblem &q, cudaStream_t stream);
 

@@ -69,6 +69,13 @@ constexpr int norm_threads(int warps) { return warps * 32 > kNormThreads ? warps
 
 constexpr int kFwdVec = 4;   // vectors a thread holds in the forward pass
 constexpr int kBwdVec = 2;   // in the backward pass (which also keeps column sums)
+// Rows in flight per thread: 24 KB of ring each for 256 threads and bf16, so
+// that two CTAs (one of 512 threads) fit an SM.
+template <typename T> constexpr int bwd_depth = sizeof(T) == 2 ? 4 : 2;
+template <typename T> constexpr size_t ring_bytes(int threads)
+{
+    return (size_t)bwd_depth<T> * 3 * kBwdVec * 8 * sizeof(T) * threads;
+}
 
 }  // namespace
 
@@ -192,16 +199,23 @@ layer_norm_kernel(const T *__restrict__ x, const T *__restrict__ residual, const
 // thread keeps its own columns of dg and db in registers over all of them;
 // the CTA's groups join in shared memory and write one partial row
 // part[cta][dg | db][cols].  The order of every sum is fixed by the launch.
+// A thread reads only what it copied itself, kDepth rows ahead, by
+// asynchronous 16-byte copies into its own places of a ring in shared memory:
+// no barrier, and no registers for what is in flight (held in registers, one
+// row ahead took 173 of them, one CTA per SM and 142 us for 32768 x 2048 bf16
+// with dsum; the bytes take 82 us).
 template <typename T, int kWarps>
-__global__ void __launch_bounds__(norm_threads(kWarps))
+__global__ void __launch_bounds__(norm_threads(kWarps), kWarps > 8 ? 1 : 2)
 layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const float *__restrict__ gamma,
                       const float *__restrict__ mean, const float *__restrict__ rstd, const T *__restrict__ dsum,
                       T *__restrict__ dx, float *__restrict__ part, long long rows, int cols)
 {
-    constexpr int kRows = norm_threads(kWarps) / (32 * kWarps);
+    constexpr int kThreads = norm_threads(kWarps), kRows = kThreads / (32 * kWarps);
+    constexpr int kPieces = sizeof(T) / 2;   // 16-byte pieces of a vector
+    constexpr int kDepth = bwd_depth<T>;
     __shared__ float2 red[2][kRows][kWarps];
-    extern __shared__ float joined[];   // [kRows - 1][2][cols]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ __align__(16) uint4 ring[];   // [kDepth][h, dy, dsum][kBwdVec][kPieces][thread]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int slot = warp / kWarps, rw = warp % kWarps;
     const int vecs = cols >> 3;
     const int v0 = rw * 32 + lane;
@@ -215,37 +229,57 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
         for (int q = 0; q < 8; ++q) g[i][q] = dg[i][q] = db[i][q] = 0.0f;
         if (e < vecs) Vec8<float>::load(gamma + 8 * e, g[i]);
     }
-    Raw8<T> rh[kBwdVec], rd[kBwdVec], rs[kBwdVec];
-    float m = 0.0f, s = 0.0f;
-    auto fetch = [&](long long row) {
+    auto place = [&](int d, int t, int i) { return ring + (((d * 3 + t) * kBwdVec + i) * kPieces) * kThreads + tid; };
+    auto copy = [&](int d, int t, int i, const T *src) {
 #pragma unroll
-        for (int i = 0; i < kBwdVec; ++i) {
-            const int e = v0 + 32 * kWarps * i;
-            if (e < vecs) {
-                rh[i].load(h + row * cols + 8 * e);
-                rd[i].load(dy + row * cols + 8 * e);
-                if (dsum) rs[i].load(dsum + row * cols + 8 * e);
+        for (int j = 0; j < kPieces; ++j)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         ::"r"((uint32_t)__cvta_generic_to_shared(place(d, t, i) + j * kThreads)),
+                         "l"(reinterpret_cast<const uint4 *>(src) + j) : "memory");
+    };
+    auto fetch = [&](long long row, int d) {
+        if (row < rows) {
+#pragma unroll
+            for (int i = 0; i < kBwdVec; ++i) {
+                const int e = v0 + 32 * kWarps * i;
+                if (e < vecs) {
+                    copy(d, 0, i, h + row * cols + 8 * e);
+                    copy(d, 1, i, dy + row * cols + 8 * e);
+                    if (dsum) copy(d, 2, i, dsum + row * cols + 8 * e);
+                }
             }
         }
-        m = mean[row];
-        s = rstd[row];
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto take = [&](int d, int t, int i, float (&v)[8]) {
+        Raw8<T> r;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) r.r[j] = place(d, t, i)[j * kThreads];
+        r.get(v);
     };
     const long long stride = (long long)gridDim.x * kRows;
     long long row = (long long)blockIdx.x * kRows + slot;
-    if (row < rows) fetch(row);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) fetch(row + d * stride, d);
+    float m = 0.0f, s = 0.0f;
+    if (row < rows) {
+        m = mean[row];
+        s = rstd[row];
+    }
+    int d = 0;
     for (int it = 0; row < rows; row += stride, it ^= 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
         float z[kBwdVec][8], a[kBwdVec][8], sv[kBwdVec][8];
         const float rs_row = s;
         float sa = 0.0f, saz = 0.0f;
 #pragma unroll
         for (int i = 0; i < kBwdVec; ++i) {
-            const bool in = v0 + 32 * kWarps * i < vecs;
 #pragma unroll
             for (int q = 0; q < 8; ++q) z[i][q] = a[i][q] = sv[i][q] = 0.0f;
-            if (!in) continue;
-            rh[i].get(z[i]);
-            rd[i].get(a[i]);
-            if (dsum) rs[i].get(sv[i]);
+            if (v0 + 32 * kWarps * i >= vecs) continue;
+            take(d, 0, i, z[i]);
+            take(d, 1, i, a[i]);
+            if (dsum) take(d, 2, i, sv[i]);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 z[i][q] = (z[i][q] - m) * s;
@@ -256,7 +290,12 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
                 saz = fmaf(a[i][q], z[i][q], saz);
             }
         }
-        if (row + stride < rows) fetch(row + stride);   // the next row's loads run under this row's sums
+        fetch(row + kDepth * stride, d);   // (this row's values have been read)
+        d = d + 1 == kDepth ? 0 : d + 1;
+        if (row + stride < rows) {
+            m = mean[row + stride];
+            s = rstd[row + stride];
+        }
         sa = warp_sum(sa);
         saz = warp_sum(saz);
         if constexpr (kWarps > 1) {
@@ -283,6 +322,9 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
             Vec8<T>::store(dx + row * cols + 8 * e, o);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float *joined = reinterpret_cast<float *>(ring);   // [kRows - 1][2][cols]
+    __syncthreads();
     if constexpr (kRows > 1) {
         if (slot > 0) {
             float *j = joined + (size_t)(slot - 1) * 2 * cols;
@@ -363,14 +405,14 @@ int warps_per_row(int cols, int vec)
     return w;
 }
 
-constexpr int kBwdCtas = 2 * 148;   // two CTAs per SM
-
+// CTAs of the backward pass: what the SMs hold (two of 256 threads, one of
+// 512), fewer where there are fewer rows.
 int bwd_ctas(long long rows, int cols)
 {
     const int w = warps_per_row(cols, kBwdVec);
-    const int per = norm_threads(w) / (32 * w);
+    const int per = norm_threads(w) / (32 * w), most = 148 * (w > 8 ? 1 : 2);
     const long long need = (rows + per - 1) / per;
-    return (int)(need < kBwdCtas ? need : kBwdCtas);
+    return (int)(need < most ? need : most);
 }
 
 template <typename T, int kWarps>
@@ -389,14 +431,18 @@ cudaError_t launch_bwd(const NormBackwardProblem &q, cudaStream_t stream)
 {
     constexpr int kRows = norm_threads(kWarps) / (32 * kWarps);
     const int ctas = bwd_ctas(q.rows, q.cols);
-    const size_t smem = (size_t)(kRows - 1) * 2 * q.cols * sizeof(float);
+    // (the rows that join need at most 28 KB of it)
+    constexpr size_t smem = ring_bytes<T>(norm_threads(kWarps));
+    static_assert((size_t)(kRows - 1) * 2 * 256 * kWarps * kBwdVec * sizeof(float) <= smem, "join");
     float *part = static_cast<float *>(q.workspace);
+    cudaError_t e = cudaFuncSetAttribute(layer_norm_bwd_kernel<T, kWarps>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     if (ctas > 0) {   // (no rows: the sums are empty)
         layer_norm_bwd_kernel<T, kWarps><<<ctas, norm_threads(kWarps), smem, stream>>>(
             static_cast<const T *>(q.dy), static_cast<const T *>(q.h), q.gamma, q.mean, q.rstd,
             static_cast<const T *>(q.dsum), static_cast<T *>(q.dx), part, q.rows, q.cols);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         count_launch();
     }
     layer_norm_join_kernel<<<dim3((q.cols + 31) / 32, q.dbeta ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(

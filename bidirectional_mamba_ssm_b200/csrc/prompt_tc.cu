@@ -93,7 +93,8 @@ struct PromptParams {
     int *status;
     int batch, len, H, ch, pool;
     int max_chunks;          // chunks of the operand array
-    int seg_chunks;          // prompts above this are cut
+    int cut_over;            // prompts of more chunks are cut
+    int seg_chunks;          // into pieces of at most this many
 };
 
 // Prompt s as the plan sees it: its chunks, or none where its slot or range
@@ -188,6 +189,8 @@ __device__ __forceinline__ void tmem_st4_nw(uint32_t taddr, const uint32_t *r)
 __global__ void __launch_bounds__(kPrepThreads)
 prompt_prep_kernel(const PromptParams p)
 {
+    // the walk kernel behind this one may start its set-up
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
     const int me = blockIdx.x;
     if (me == p.max_chunks) {
@@ -198,11 +201,11 @@ prompt_prep_kernel(const PromptParams p)
         int inner = 0, chunks = 0;
         int cls[4] = {0, 0, 0, 0};
         auto shape = [&](const Prompt &r, int &nseg, int &seg) {
-            nseg = r.chunks > p.seg_chunks ? (r.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
+            nseg = r.chunks > p.cut_over ? (r.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
             seg = nseg > 1 ? (r.chunks + nseg - 1) / nseg : r.chunks;
             if (nseg > 1) nseg = (r.chunks + seg - 1) / seg;
         };
-        auto class_of = [&](int n) { return min(3, 4 * n / (p.seg_chunks + 1)); };
+        auto class_of = [&](int n) { return min(3, 4 * n / (p.cut_over + 1)); };
         for (int s0 = 0; s0 < p.batch; s0 += kPrepThreads) {
             Prompt r = read_prompt(p, s0 + tid);
             if (r.bad) record_error(p.status, kStatusBadSlot);
@@ -345,6 +348,7 @@ prompt_prep_kernel(const PromptParams p)
 __global__ void __launch_bounds__(256)
 prompt_chain_kernel(const PromptParams p)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int s = blockIdx.y;
     const int2 seg = p.segs[s];
     if (seg.y <= 1) return;
@@ -516,6 +520,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int H = p.H, ch = p.ch, HP = H / 2;
     const int hp = blockIdx.x % HP;
     const int wi = blockIdx.x / HP;
+    // (a programmatic launch: everything read below was written by kernels
+    // before this one)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (wi >= (kStateOnly ? p.head->inner : p.head->total)) return;
     const Walk wk = p.walks[wi];
     const int slot = p.slots[wk.seq];
@@ -1319,24 +1326,42 @@ namespace {
 constexpr int kSMs = 148;
 
 struct Layout {
-    int max_chunks, seg_chunks, max_inner, max_walks, max_slots;
+    int max_chunks, cut_over, seg_chunks, max_inner, max_walks, max_slots;
     size_t head, walks, segs, act, dec, state, bytes;
 };
 
+// How prompts are cut.  A prompt is cut once its walk would take a fifth
+// longer than the GPU's average share of the call (cut_over chunks; never
+// below 4).  The pieces are as long as is best for one prompt of all the
+// rows: n pieces take ceil(n pairs / SMs) rounds of a piece's chunks, after
+// state-only walks of the first n - 1 at about half the time a chunk.
+void cut_of(long long chunks, int pairs, int &cut_over, int &seg_chunks)
+{
+    const long long share = (chunks * pairs + kSMs - 1) / kSMs;
+    cut_over = (int)std::max<long long>(4, (share * 6 + 4) / 5);
+    long long best = 1ll << 60;
+    seg_chunks = cut_over;
+    for (long long n = 2; n <= 16 && n <= chunks; ++n) {
+        const long long seg = (chunks + n - 1) / n;
+        const long long cost = seg * (2 * ((n * pairs + kSMs - 1) / kSMs) + ((n - 1) * pairs + kSMs - 1) / kSMs);
+        if (cost < best) {
+            best = cost;
+            seg_chunks = (int)seg;
+        }
+    }
+    seg_chunks = std::min(seg_chunks, cut_over);
+}
+
 // Sizes that hold for any lengths of `batch` prompts in `len` rows: a prompt
-// of L tokens has at most L / 128 + 1 chunks.
+// of L tokens has at most L / 128 + 1 chunks, and a cut one c / seg_chunks + 1
+// pieces.
 Layout layout_of(const bimamba_dims &d)
 {
     Layout l{};
     const long long chunks = (long long)d.len / kQ + std::min(d.batch, d.len);
     l.max_chunks = (int)chunks;
-    // A prompt is cut once it exceeds a fifth more than the GPU's average
-    // share of the call's chunks, but never below 4 chunks: the state-only
-    // walks and the chain cost about half of the walk that they let run in
-    // parallel.
-    const long long share = ((long long)d.len / kQ * (d.heads / 2) + kSMs - 1) / kSMs;
-    l.seg_chunks = (int)std::max<long long>(4, (share * 6 + 4) / 5);
-    const bool cut = d.len > l.seg_chunks * (long long)kQ;
+    cut_of((long long)d.len / kQ, d.heads / 2, l.cut_over, l.seg_chunks);
+    const bool cut = d.len > l.cut_over * (long long)kQ;
     l.max_inner = cut ? (int)(chunks / l.seg_chunks) : 0;
     l.max_walks = l.max_inner + d.batch;
     l.max_slots = 2 * l.max_inner;
@@ -1404,6 +1429,7 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
     p.status = q.status;
     p.batch = d.batch; p.len = d.len; p.H = d.heads; p.ch = d.heads * kP + 2 * kN; p.pool = q.pool;
     p.max_chunks = l.max_chunks;
+    p.cut_over = l.cut_over;
     p.seg_chunks = l.seg_chunks;
 
     CUtensorMap tm_x, tm_bc, tm_y;
@@ -1431,8 +1457,17 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         count_launch(2);
     }
-    prompt_walk_kernel<false><<<(unsigned)pairs * l.max_walks, kThreads, kSmemBytes, stream>>>(tm_x, tm_bc, tm_y, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pairs * l.max_walks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, prompt_walk_kernel<false>, tm_x, tm_bc, tm_y, p)) != cudaSuccess) return e;
     count_launch();
     return cudaSuccess;
 }

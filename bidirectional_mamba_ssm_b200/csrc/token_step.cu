@@ -32,7 +32,7 @@ constexpr int kStepLoads = 8;   // 16-byte state loads a thread keeps in flight
 // rewritten by the last of them to have read (a ticket per row in the
 // workspace, returned to zero by that CTA); nobody waits for it.
 template <typename T, int N>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, 3)
 token_step_kernel(const StepProblem q)
 {
     constexpr int kRowVecs = N / 4;                       // float4s of one state row
@@ -46,14 +46,11 @@ token_step_kernel(const StepProblem q)
     const int h = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
     const int P = q.P, ch = q.H * P + 2 * N;
     const int slot = q.slots[row];
-    // a row whose slot is not one of the pool's, or is another row's too, is
-    // skipped (a negative one without an error: a padding row)
-    bool twice = false;
-    if (slot >= 0)
-        for (int r = tid; r < q.rows; r += kStepThreads) twice |= r != row && q.slots[r] == slot;
     const int col = tid % kLanes, prow = tid / kLanes;
     const bool in_pool = slot >= 0 && slot < q.pool;
     float4 *state = reinterpret_cast<float4 *>(q.state + ((size_t)(in_pool ? slot : 0) * q.H + h) * P * N);
+    T *tail = static_cast<T *>(q.tail) + (size_t)(in_pool ? slot : 0) * 4 * ch;
+    const T *raw = static_cast<const T *>(q.xbc) + (size_t)row * ch;
     float4 s[kPasses][kPer];
     auto fetch = [&](int p0) {
 #pragma unroll
@@ -64,30 +61,55 @@ token_step_kernel(const StepProblem q)
                 if (p < P) s[i][k] = state[(size_t)p * kRowVecs + col + kLanes * k];
         }
     };
-    if (in_pool) fetch(0);
+    // this thread's conv channels, requested right behind the state
+    constexpr int kConv = (128 + 2 * N + kStepThreads - 1) / kStepThreads;
+    T t[kConv][4];
+    float4 w[kConv];
+    float bias[kConv];
+    auto channel = [&](int i) { return i < P ? h * P + i : q.H * P + (i - P); };
+    if (in_pool) {
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < kConv; ++j) {
+            const int i = tid + j * kStepThreads;
+            if (i < P + 2 * N) {
+                const int c = channel(i);
+                t[j][0] = tail[ch + c];
+                t[j][1] = tail[2 * ch + c];
+                t[j][2] = tail[3 * ch + c];
+                t[j][3] = raw[c];
+                w[j] = *reinterpret_cast<const float4 *>(q.conv_w + (size_t)c * 4);
+                bias[j] = q.conv_b ? q.conv_b[c] : 0.0f;
+            }
+        }
+    }
+    // a row whose slot is not one of the pool's, or is another row's too, is
+    // skipped (a negative one without an error: a padding row)
+    bool twice = false;
+    if (slot >= 0)
+        for (int r = tid; r < q.rows; r += kStepThreads) twice |= r != row && q.slots[r] == slot;
     twice = __syncthreads_or(twice);
     if (!in_pool || twice) {
         if (slot >= 0 && h == 0 && tid == 0) record_error(q.status, kStatusBadSlot);
         return;
     }
 
-    T *tail = static_cast<T *>(q.tail) + (size_t)slot * 4 * ch;
-    const T *raw = static_cast<const T *>(q.xbc) + (size_t)row * ch;
-    for (int i = tid; i < P + 2 * N; i += kStepThreads) {
-        const int c = i < P ? h * P + i : q.H * P + (i - P);
-        const float4 w = *reinterpret_cast<const float4 *>(q.conv_w + (size_t)c * 4);
-        const T t1 = tail[ch + c], t2 = tail[2 * ch + c], t3 = tail[3 * ch + c], t4 = raw[c];
-        float a = q.conv_b ? q.conv_b[c] : 0.0f;
-        a = fmaf(w.x, static_cast<float>(t1), a);
-        a = fmaf(w.y, static_cast<float>(t2), a);
-        a = fmaf(w.z, static_cast<float>(t3), a);
-        a = fmaf(w.w, static_cast<float>(t4), a);
+#pragma unroll
+    for (int j = 0; j < kConv; ++j) {
+        const int i = tid + j * kStepThreads;
+        if (i >= P + 2 * N) break;
+        float a = bias[j];
+        a = fmaf(w[j].x, static_cast<float>(t[j][0]), a);
+        a = fmaf(w[j].y, static_cast<float>(t[j][1]), a);
+        a = fmaf(w[j].z, static_cast<float>(t[j][2]), a);
+        a = fmaf(w[j].w, static_cast<float>(t[j][3]), a);
         act[i] = silu_f(a);
         if (i < P) {   // this head's own channels
-            tail[c] = t1;
-            tail[ch + c] = t2;
-            tail[2 * ch + c] = t3;
-            tail[3 * ch + c] = t4;
+            const int c = channel(i);
+            tail[c] = t[j][0];
+            tail[ch + c] = t[j][1];
+            tail[2 * ch + c] = t[j][2];
+            tail[3 * ch + c] = t[j][3];
         }
     }
     const float dt = Elem<T>::load(static_cast<const T *>(q.dt) + (size_t)row * q.H + h);

@@ -378,9 +378,8 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
  *                resumes leaves its entry as it is, one that does not zeroes it.
  *   y          : (len, H*P) dtype
  *   workspace  : bimamba_prompt_workspace_bytes(d) bytes, 256-byte aligned,
- *                zero-filled before its first use; a call leaves it fit for
- *                the next call with any dims it is large enough for.  Calls
- *                that share one (two graphs, too) must not run concurrently.
+ *                no clearing needed.  Calls that share one (two graphs, too)
+ *                must not run concurrently.
  * What only the device knows is checked there: a prompt whose slot is
  * outside [0, pool_size) or is another prompt's too, or whose rows are not a
  * range inside [0, len), is skipped (y and the pool untouched) and makes
@@ -405,8 +404,9 @@ int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, 
  *   y    : (batch, H*P) dtype
  *   the others as in bimamba_prompt_scan; workspace:
  *   bimamba_token_step_workspace_bytes(d) bytes, zero-filled before its
- *   first use (same rules).  Row s's result equals a prompt of one token
- *   that resumes.  Bad, repeated and negative slots as there.
+ *   first use; a call leaves it fit for the next, of any dims it is large
+ *   enough for (the same rule on sharing).  Row s's result equals a prompt of
+ *   one token that resumes.  Bad, repeated and negative slots as there.
  */
 size_t bimamba_token_step_workspace_bytes(const bimamba_dims *d);
 
