@@ -69,9 +69,10 @@ constexpr int norm_threads(int warps) { return warps * 32 > kNormThreads ? warps
 
 constexpr int kFwdVec = 4;   // vectors a thread holds in the forward pass
 constexpr int kBwdVec = 2;   // in the backward pass (which also keeps column sums)
-// Rows in flight per thread: 24 KB of ring each for 256 threads and bf16, so
-// that two CTAs (one of 512 threads) fit an SM.
-template <typename T> constexpr int bwd_depth = sizeof(T) == 2 ? 4 : 2;
+// Rows in flight per thread (24 KB of ring each for 256 threads and bf16; two
+// CTAs an SM, one of 512 threads).  32768 x 2048 bf16: 4 rows 105 us, 3 or 2
+// 102 us.
+template <typename T> constexpr int bwd_depth = sizeof(T) == 2 ? 3 : 2;
 template <typename T> constexpr size_t ring_bytes(int threads)
 {
     return (size_t)bwd_depth<T> * 3 * kBwdVec * 8 * sizeof(T) * threads;
@@ -210,6 +211,8 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
                       const float *__restrict__ mean, const float *__restrict__ rstd, const T *__restrict__ dsum,
                       T *__restrict__ dx, float *__restrict__ part, long long rows, int cols)
 {
+    // the join kernel behind this one may take its place as CTAs end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kThreads = norm_threads(kWarps), kRows = kThreads / (32 * kWarps);
     constexpr int kPieces = sizeof(T) / 2;   // 16-byte pieces of a vector
     constexpr int kDepth = bwd_depth<T>;
@@ -374,6 +377,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 layer_norm_join_kernel(const float *__restrict__ part, float *__restrict__ dgamma, float *__restrict__ dbeta,
                        int nparts, int cols)
 {
+    // (a programmatic launch: the partial rows are complete after this)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sums[kJoinWarps][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
@@ -445,9 +450,17 @@ cudaError_t launch_bwd(const NormBackwardProblem &q, cudaStream_t stream)
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         count_launch();
     }
-    layer_norm_join_kernel<<<dim3((q.cols + 31) / 32, q.dbeta ? 2 : 1), 32 * kJoinWarps, 0, stream>>>(
-        part, q.dgamma, q.dbeta, ctas, q.cols);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((q.cols + 31) / 32, q.dbeta ? 2 : 1);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, layer_norm_join_kernel, static_cast<const float *>(part), q.dgamma, q.dbeta, ctas,
+                              q.cols);
 }
 
 }  // namespace
