@@ -396,8 +396,8 @@ constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]
 constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][part][128]: first token of X not finite (128: none)
 constexpr uint32_t kOffAnyBad = kOffBad + 2 * kParts * kPP;   // int [2 parity][X, M group]
 constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
-constexpr uint32_t kOffTaps = kOffDtBuf + 2 * kQ * 4;   // float4 [128] conv taps, float [128] biases, float [2] D
-constexpr uint32_t kOffMbar = kOffTaps + kPP * 20 + 8;
+constexpr uint32_t kOffTaps = kOffDtBuf + 2 * kQ * 4;   // float4 [128] conv taps, float [128] biases, float [2] D, float [3][128] halo
+constexpr uint32_t kOffMbar = kOffTaps + kPP * 20 + 8 + 3 * kPP * 4;
 constexpr uint32_t kOffTmem = kOffMbar + 160;
 
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
@@ -416,7 +416,7 @@ constexpr int kYWarp = 8, kXWarp = 16, kProducerWarp = 28, kHelperWarp = 29, kPu
 constexpr int kThreads = 32 * 32;
 // registers a thread: 1024 threads are launched with 64; the Y group holds
 // the state (64 values a thread)
-constexpr int kRegsLaunch = 64, kRegsM = 64, kRegsY = 96, kRegsX = 48, kRegsOne = 48;
+constexpr int kRegsLaunch = 64, kRegsM = 56, kRegsY = 96, kRegsX = 56, kRegsOne = 40;
 static_assert(kRegsM * kMGroup + kRegsY * kYGroup + kRegsX * kXGroup + kRegsOne * 128 <= kRegsLaunch * kThreads, "register shares");
 
 template <int kRegs> __device__ __forceinline__ void take_registers()
@@ -570,8 +570,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     auto phase = [](int k) -> uint32_t { return (k >> 1) & 1; };   // of a pair's barrier
     auto xbuf = [](int k) { return (k & 1) ? kOffX1 : kOffX0; };
     // chunk k's rows in the prompt
-    auto tokens = [&](int k) { return min(kQ, len - (wk.chunk + k) * kQ); };
-    auto first_row = [&](int k) { return begin + (wk.chunk + k) * kQ; };
+    const int left = len - wk.chunk * kQ, row0 = begin + wk.chunk * kQ;
+    auto tokens = [&](int k) { return min(kQ, left - k * kQ); };
+    auto first_row = [&](int k) { return row0 + k * kQ; };
 
     auto issue_x = [&](int k) {
         tc::mbar_expect_tx(mb_x, kRawBytes);
@@ -618,6 +619,12 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         biases[tid] = p.conv_b ? p.conv_b[hp * kPP + tid] : 0.0f;
     }
     if (tid < 2) biases[kPP + tid] = p.D[2 * hp + tid];
+    // the 3 tokens before the walk's first chunk where they are not in the raw
+    // tile: the prompt's entry's tail, or zeros
+    const bool starts = wk.chunk == 0;
+    float *halo = biases + kPP + 2;   // [3][128]
+    if (starts && tid < 3 * kPP)
+        halo[tid] = resume ? __bfloat162float(tail[(1 + tid / kPP) * ch + hp * kPP + tid % kPP]) : 0.0f;
     if (warp == 0) tc::tmem_alloc(sbase + kOffTmem, 512);
     if (tid == 32 * kProducerWarp) {
         tc::prefetch_tmap(&tm_x);
@@ -671,12 +678,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         };
         const int rows = tokens(k) + 3;   // rows past these are a neighbour's
         float v0 = ld(8 * ua), v1 = ld(8 * ua + 1), v2 = ld(8 * ua + 2);
-        if (ua == 0 && k == 0 && wk.chunk == 0) {
-            // the 3 tokens before the prompt: its entry's tail, or zeros
-            const __nv_bfloat16 *t = tail + hp * kPP + pr;
-            v0 = resume ? __bfloat162float(t[ch]) : 0.0f;
-            v1 = resume ? __bfloat162float(t[2 * ch]) : 0.0f;
-            v2 = resume ? __bfloat162float(t[3 * ch]) : 0.0f;
+        if (ua == 0 && k == 0 && starts) {
+            v0 = halo[pr];
+            v1 = halo[kPP + pr];
+            v2 = halo[2 * kPP + pr];
         } else {
             if (8 * ua >= rows) v0 = 0.0f;
             if (8 * ua + 1 >= rows) v1 = 0.0f;
@@ -1017,7 +1022,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     const int U = h * quad + i;
                     tc::tmem_ld16_nw(gcol + 16 * U, g);
                     tc::tmem_wait_ld16(g);
-#pragma unroll
+#pragma unroll 1
                     for (int hd = 0; hd < 2; ++hd) {
                         const float *cm = c0 + hd * kQ;
                         const float et = tc::exp2_approx(cm[row] - cm[16 * U | 31]);
@@ -1041,6 +1046,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 tc::tmem_wait_ld16(g);
                 // the diagonal block's unit: column s = 16 h + i against row r of the block
                 const int r = (row & 31) - 16 * h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i > r) g[i] = 0u;
 #pragma unroll 1
                 for (int hd = 0; hd < 2; ++hd) {
                     const float *cb = c0 + hd * kQ + 32 * quad;   // the block's
@@ -1055,21 +1063,21 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float rf = tc::exp2_approx(ct - cm[4 * j + 3]);
+                            const float2 rf2 = make_float2(rf, rf);
                             const float4 f = f4h[j];
-                            const float fs[4] = {f.x, f.y, f.z, f.w};
-                            float v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int i = 4 * j + e;
-                                const float x = fmaf(__uint_as_float(g[i]) * rf, fs[e], i == r ? Dh : 0.0f);
-                                v[e] = i <= r ? x : 0.0f;
-                            }
-                            out[2 * j] = tc::pack_bf16x2(v[0], v[1]);
-                            out[2 * j + 1] = tc::pack_bf16x2(v[2], v[3]);
+                            const float2 a = tc::fma2(tc::mul2(make_float2(__uint_as_float(g[4 * j]), __uint_as_float(g[4 * j + 1])), rf2),
+                                                      make_float2(f.x, f.y),
+                                                      make_float2(4 * j == r ? Dh : 0.0f, 4 * j + 1 == r ? Dh : 0.0f));
+                            const float2 b = tc::fma2(tc::mul2(make_float2(__uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3])), rf2),
+                                                      make_float2(f.z, f.w),
+                                                      make_float2(4 * j + 2 == r ? Dh : 0.0f, 4 * j + 3 == r ? Dh : 0.0f));
+                            out[2 * j] = tc::pack_bf16x2(a.x, a.y);
+                            out[2 * j + 1] = tc::pack_bf16x2(b.x, b.y);
                         }
                     } else {
-                        // steep decays (or a dt that is not finite): one
-                        // exponential per element, each <= 1
+                        // steep decays (or a dt that is not finite, whose
+                        // factors must not meet the zeros): one exponential per
+                        // element, each <= 1
                         const float *dh = cm + (kOffDt - kOffCum) / 4;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -1259,16 +1267,21 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (tb == 0) tc::mbar_arrive(mb_st);
             }
         }
-        if (ok && (kStateOnly || wk.last) && (nk > 0 || !resume)) {
-            // the state after the walk (an empty prompt that resumes keeps its entry)
-            float *to = kStateOnly ? p.seg_state + (size_t)(wk.slot + 1) * H * kP * kN + pair_off
-                                   : p.state + (size_t)slot * H * kP * kN + pair_off;
+        // the state after the walk (an empty prompt that resumes keeps its
+        // entry).  Its place is looked up again: not a register is spared for
+        // it through the loop.
+        const Walk end = p.walks[blockIdx.x / HP];
+        const bool again = p.resume && p.resume[end.seq] != 0;
+        if (ok && (kStateOnly || end.last) && (nk > 0 || !again)) {
+            const size_t off = (size_t)hp * kPP * kN + (size_t)prow * kN + 64 * hf;
+            float *to = kStateOnly ? p.seg_state + (size_t)(end.slot + 1) * H * kP * kN + off
+                                   : p.state + (size_t)p.slots[end.seq] * H * kP * kN + off;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 *reinterpret_cast<float4 *>(to + 4 * i) =
                     make_float4(st[2 * i].x, st[2 * i].y, st[2 * i + 1].x, st[2 * i + 1].y);
             if (kStateOnly && hf == 0 && (prow & 63) == 0)
-                p.seg_dec[(size_t)(wk.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
+                p.seg_dec[(size_t)(end.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
         }
         if (!ok && tb == 0) record_error(p.status, kStatusTimeout);
     } else if (warp < kProducerWarp) {
@@ -1297,17 +1310,21 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     if constexpr (!kStateOnly) {
         // the new tail: by the prompt's first walk (the only one that read the
         // old x channels; the old B and C channels were read by the prep kernel)
-        if (wk.chunk == 0) {
+        if (starts) {
+            const int seq = p.walks[blockIdx.x / HP].seq;
+            const bool again = p.resume && p.resume[seq] != 0;
+            const int from = p.cu[seq], n = p.cu[seq + 1] - from;
+            __nv_bfloat16 *entry = p.tail + (size_t)p.slots[seq] * 4 * ch;
             auto commit = [&](int cc) {
                 __nv_bfloat16 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int t = len - 4 + i;
-                    v[i] = t >= 0 ? p.xbc[(size_t)(begin + t) * ch + cc]
-                                  : resume ? tail[(size_t)(4 + t) * ch + cc] : __float2bfloat16_rn(0.0f);
+                    const int t = n - 4 + i;
+                    v[i] = t >= 0 ? p.xbc[(size_t)(from + t) * ch + cc]
+                                  : again ? entry[(size_t)(4 + t) * ch + cc] : __float2bfloat16_rn(0.0f);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tail[(size_t)i * ch + cc] = v[i];
+                for (int i = 0; i < 4; ++i) entry[(size_t)i * ch + cc] = v[i];
             };
             if (tid < kPP) commit(hp * kPP + tid);
             else if (hp == 0 && tid < kPP + 2 * kN) commit(H * kP + tid - kPP);
