@@ -9,6 +9,8 @@ the shared library.
 __all__ = ["bimamba_version", "bimamba_launch_count", "bimamba_set_timing_events", "bimamba_strerror", "bimamba_get_error", "bimamba_conv_silu",
            "bimamba_workspace_bytes", "bimamba_ssd_fwd_rev", "bimamba_block_decode",
            "make_dims", "new_workspace", "BimambaError",
+           "bimamba_prompt_scan", "new_prompt_workspace", "bimamba_token_step", "new_step_workspace",
+           "bimamba_layer_norm", "bimamba_layer_norm_backward", "new_layer_norm_workspace",
            "bimamba_noalloc_scratch_bytes", "bimamba_block_decode_noalloc"]
 
 

@@ -496,7 +496,7 @@ static int check_causal(const bimamba_dims *d, const void *xbc, const void *dt, 
 
 size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d)
 {
-    if (check_dims(d) != BIMAMBA_OK) return 0;
+    if (check_dims(d) != BIMAMBA_OK || d->len > (1 << 30)) return 0;
     // (256 bytes at least: a workspace is always wanted)
     const size_t n = prompt_tc_supported(*d) ? prompt_tc_ws_bytes(*d) : prompt_seq_ws_bytes(*d);
     return (n + 511) & ~(size_t)255;
@@ -510,6 +510,7 @@ int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, 
 {
     int st = check_dims(d);
     if (st != BIMAMBA_OK) return st;
+    if (d->len > (1 << 30)) return BIMAMBA_ERR_UNSUPPORTED;   // (32-bit operand rows)
     if (d->batch == 0) return BIMAMBA_OK;
     if (!cu_seqlens) return BIMAMBA_ERR_INVALID;
     st = check_causal(d, xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, tail_pool, pool_size,

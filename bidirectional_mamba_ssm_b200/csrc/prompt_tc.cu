@@ -427,10 +427,11 @@ template <int kRegs> __device__ __forceinline__ void take_registers()
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// Bounded wait for phase `parity` of `bar`: false after kWaitTries tries (two
-// seconds and more).  Three instructions a try: the waiting threads of a walk
-// poll beside the warps that compute.
-constexpr uint32_t kWaitTries = 1u << 26;
+// Bounded wait for phase `parity` of `bar`: false after kWaitTries tries (a
+// try that finds the phase incomplete takes some tens of cycles: half a second
+// and more, where the longest wait of a walk is tens of microseconds).  Three
+// instructions a try: the waiting threads poll beside the warps that compute.
+constexpr uint32_t kWaitTries = 1u << 24;
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 {

@@ -269,3 +269,83 @@ def test_the_pool_feeds_the_block_decode(lib):
     for k in slots.tolist():
         assert ref.far(st[k], end_s[k]) <= 6e-3              # the block decode's state operands are bf16
         np.testing.assert_array_equal(to_np(tl[k]), end_t[k])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("where", ["x", "B", "C", "dt"])
+@pytest.mark.parametrize("at", [0, 5, 127, 130])
+def test_a_bad_token_leaves_the_rows_before_it(lib, dtype, where, at):
+    """An infinity or NaN enters the outputs at its own token, not before
+    (although the tokens of a 128-row tile share their products), and in x
+    only its own channel."""
+    shape, n = (2, 64, 128), 200
+    H, P, N = shape
+    d = ref.draw(n, 1, *shape, dtype, seed=9, pool=1)
+    y0, _, _ = ref.run(lib, d, [n], [1], *shape)
+    for value in (float("nan"), float("inf")):
+        bad = dict(d, xbc=d["xbc"].clone(), dt=d["dt"].clone())
+        if where == "dt":
+            bad["dt"][at, 1] = value
+        else:
+            bad["xbc"][at, {"x": 70, "B": H * P + 3, "C": H * P + N + 3}[where]] = value
+        y1, s1, _ = ref.run(lib, bad, [n], [1], *shape)
+        assert torch.equal(y0[:at], y1[:at])
+        if where == "x":
+            rest = [c for c in range(H * P) if c != 70]
+            assert torch.equal(y0[:, rest], y1[:, rest])
+            assert not torch.isfinite(y1[at:, 70]).any()
+            assert not torch.isfinite(s1[0, 1, 6]).any() and torch.isfinite(s1[0, 1, 7]).all()
+        elif where == "C":
+            assert not torch.isfinite(y1[at]).any() and torch.isfinite(y1[at + 4:]).all()
+        elif where == "dt":
+            assert torch.equal(y0[:, :64], y1[:, :64])       # the other head
+            assert not torch.isfinite(y1[at:, 64:]).any()
+        else:
+            assert not torch.isfinite(y1[at:]).any()
+    assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_rows_at_all(lib, dtype):
+    """A batch of empty prompts: entries that resume stay, the others are zeroed."""
+    shape = (2, 64, 128)
+    d = ref.draw(0, 3, *shape, dtype, seed=1, pool=4)
+    _, s, t = ref.run(lib, d, [0, 0, 0], [1, 0, 1], *shape)
+    assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+    k = int(d["slots"][1])
+    keep = [i for i in range(4) if i != k]
+    assert torch.equal(s[keep].cpu(), d["state"][keep]) and torch.equal(t[keep].cpu(), d["tail"][keep])
+    assert not s[k].any() and not t[k].any()
+
+
+@pytest.mark.parametrize("a_range", [(200.0, 400.0), (1e-6, 1e-5)])
+def test_extreme_decays(lib, a_range):
+    """Decays that leave nothing of a token two tokens on, and ones that lose
+    nothing over a thousand."""
+    shape, lens = (2, 64, 128), [300, 1000]
+    d = ref.draw(sum(lens), 2, *shape, torch.bfloat16, seed=12, pool=2, a_range=a_range)
+    _check(lib, d, lens, [1, 0], shape)
+
+
+def test_many_prompts(lib):
+    """More prompts than a plan pass takes at once, most of them empty or short."""
+    shape, n = (2, 64, 128), 700
+    lens = [(7 * i) % 5 if i % 9 else 130 for i in range(n)]
+    d = ref.draw(sum(lens), n, *shape, torch.bfloat16, seed=13, pool=n + 1)
+    _check(lib, d, lens, [i % 2 for i in range(n)], shape)
+
+
+def test_larger_batch_of_the_model_shape(lib):
+    """64 heads, a batch that fills the SMs more than once, against the fp32
+    kernel on the same values (which the tests above hold against 64 bits)."""
+    shape, lens = (64, 64, 128), [900, 17, 2500, 300, 1, 64, 1025, 777]
+    d = ref.draw(sum(lens), len(lens), *shape, torch.bfloat16, seed=14, pool=len(lens))
+    res = [i % 2 for i in range(len(lens))]
+    y, s, t = ref.run(lib, d, lens, res, *shape)
+    f = dict(d, xbc=d["xbc"].float(), dt=d["dt"].float(), tail=d["tail"].float())
+    fy, fs, ft = ref.run(lib, f, lens, res, *shape)
+    assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+    assert ref.far(y, to_np(fy)) <= Y_TOL[torch.bfloat16]
+    for k in range(len(lens)):
+        assert ref.far(s[k], to_np(fs[k])) <= 2 * STATE_TOL
+    assert torch.equal(t.float(), ft)
