@@ -134,3 +134,24 @@ def test_a_large_pool(lib):
     assert torch.equal(y, want[0])
     assert torch.equal(state[pool - 1], want[1][0]) and torch.equal(state[pool - 2], want[1][1])
     assert torch.equal(tail[pool - 1], want[2][0])
+
+
+def test_thousands_of_steps_of_a_slow_decay(lib):
+    """4096 equal steps of decays near 1: two roundings a step (at most 2^-24
+    each, independent) are sqrt(8192) 2^-24 / sqrt(3) = 3e-6 of the state; a
+    decay rounded alike at every step would be some 4096 2^-25 / sqrt(3) =
+    7e-5.  1e-5."""
+    shape, n = (4, 64, 128), 4096
+    d = ref.draw(n, 1, *shape, torch.float32, seed=11, pool=1, a_range=(1e-4, 1e-2))
+    d["dt"].fill_(0.05)
+    _, want, _ = ref.prompts(d, [n], [1], *shape)
+    c = {k: v.cuda() for k, v in d.items()}
+    kw = dict(heads=4, headdim=64, d_state=128)
+    ws = lib.new_step_workspace(1, dtype=torch.float32, **kw)
+    y = torch.empty((1, 256), device="cuda")
+    for t in range(n):
+        lib.bimamba_token_step(c["xbc"][t:t + 1], c["dt"][t:t + 1], c["A"], c["D"], c["conv_w"], c["conv_b"],
+                               c["state"], c["tail"], c["slots"], y, ws, **kw)
+    assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+    for h in range(4):
+        assert ref.far(c["state"][0, h], want[0, h]) <= 1e-5, h
