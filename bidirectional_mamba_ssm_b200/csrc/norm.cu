@@ -15,6 +15,7 @@
 // `kVec` 16-byte-per-8-element vectors of it.
 #include "common.cuh"
 #include "dispatch.h"
+#include "tc_ptx.cuh"
 
 namespace bimamba {
 
@@ -27,6 +28,22 @@ template <typename T> struct Raw8 {
     {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    // as 4 packed pairs
+    __device__ __forceinline__ void get(float2 (&v)[4]) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[2 * i] = make_float2(__uint_as_float(r[i].x), __uint_as_float(r[i].y));
+                v[2 * i + 1] = make_float2(__uint_as_float(r[i].z), __uint_as_float(r[i].w));
+            }
+        } else {
+            const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
@@ -224,13 +241,16 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
     const int v0 = rw * 32 + lane;
     const float inv_cols = 1.0f / (float)cols;
 
-    float g[kBwdVec][8], dg[kBwdVec][8], db[kBwdVec][8];
+    float2 g[kBwdVec][4], dg[kBwdVec][4], db[kBwdVec][4];   // (packed pairs: the pass is near the issue rate)
+    const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
 #pragma unroll
     for (int i = 0; i < kBwdVec; ++i) {
         const int e = v0 + 32 * kWarps * i;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) g[i][q] = dg[i][q] = db[i][q] = 0.0f;
-        if (e < vecs) Vec8<float>::load(gamma + 8 * e, g[i]);
+        for (int q = 0; q < 4; ++q) {
+            dg[i][q] = db[i][q] = zero;
+            g[i][q] = e < vecs ? *reinterpret_cast<const float2 *>(gamma + 8 * e + 2 * q) : zero;
+        }
     }
     auto place = [&](int d, int t, int i) { return ring + (((d * 3 + t) * kBwdVec + i) * kPieces) * kThreads + tid; };
     auto copy = [&](int d, int t, int i, const T *src) {
@@ -254,7 +274,7 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto take = [&](int d, int t, int i, float (&v)[8]) {
+    auto take = [&](int d, int t, int i, float2 (&v)[4]) {
         Raw8<T> r;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) r.r[j] = place(d, t, i)[j * kThreads];
@@ -272,27 +292,30 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
     int d = 0;
     for (int it = 0; row < rows; row += stride, it ^= 1) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-        float z[kBwdVec][8], a[kBwdVec][8], sv[kBwdVec][8];
+        float2 z[kBwdVec][4], a[kBwdVec][4], sv[kBwdVec][4];
         const float rs_row = s;
-        float sa = 0.0f, saz = 0.0f;
+        // (h - m) s: the difference first, which is exact where it matters
+        const float2 s2 = make_float2(s, s), m2 = make_float2(-m, -m);
+        float2 sa2 = zero, saz2 = zero;
 #pragma unroll
         for (int i = 0; i < kBwdVec; ++i) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) z[i][q] = a[i][q] = sv[i][q] = 0.0f;
+            for (int q = 0; q < 4; ++q) z[i][q] = a[i][q] = sv[i][q] = zero;
             if (v0 + 32 * kWarps * i >= vecs) continue;
             take(d, 0, i, z[i]);
             take(d, 1, i, a[i]);
             if (dsum) take(d, 2, i, sv[i]);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                z[i][q] = (z[i][q] - m) * s;
-                dg[i][q] = fmaf(a[i][q], z[i][q], dg[i][q]);
-                db[i][q] += a[i][q];
-                a[i][q] *= g[i][q];
-                sa += a[i][q];
-                saz = fmaf(a[i][q], z[i][q], saz);
+            for (int q = 0; q < 4; ++q) {
+                z[i][q] = tc::mul2(tc::fma2(z[i][q], one, m2), s2);
+                dg[i][q] = tc::fma2(a[i][q], z[i][q], dg[i][q]);
+                db[i][q] = tc::fma2(a[i][q], one, db[i][q]);
+                a[i][q] = tc::mul2(a[i][q], g[i][q]);
+                sa2 = tc::fma2(a[i][q], one, sa2);
+                saz2 = tc::fma2(a[i][q], z[i][q], saz2);
             }
         }
+        float sa = sa2.x + sa2.y, saz = saz2.x + saz2.y;
         fetch(row + kDepth * stride, d);   // (this row's values have been read)
         d = d + 1 == kDepth ? 0 : d + 1;
         if (row + stride < rows) {
@@ -320,8 +343,13 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
             const int e = v0 + 32 * kWarps * i;
             if (e >= vecs) continue;
             float o[8];
+            const float2 sa_2 = make_float2(-sa, -sa), saz_2 = make_float2(-saz, -saz), rs_2 = make_float2(rs_row, rs_row);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = fmaf(rs_row, a[i][q] - sa - z[i][q] * saz, sv[i][q]);
+            for (int q = 0; q < 4; ++q) {
+                const float2 v = tc::fma2(tc::fma2(z[i][q], saz_2, tc::fma2(a[i][q], one, sa_2)), rs_2, sv[i][q]);
+                o[2 * q] = v.x;
+                o[2 * q + 1] = v.y;
+            }
             Vec8<T>::store(dx + row * cols + 8 * e, o);
         }
     }
@@ -335,8 +363,11 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
             for (int i = 0; i < kBwdVec; ++i) {
                 const int e = v0 + 32 * kWarps * i;
                 if (e < vecs) {
-                    Vec8<float>::store(j + 8 * e, dg[i]);
-                    Vec8<float>::store(j + cols + 8 * e, db[i]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        *reinterpret_cast<float2 *>(j + 8 * e + 2 * q) = dg[i][q];
+                        *reinterpret_cast<float2 *>(j + cols + 8 * e + 2 * q) = db[i][q];
+                    }
                 }
             }
         }
@@ -348,13 +379,11 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
             for (int i = 0; i < kBwdVec; ++i) {
                 const int e = v0 + 32 * kWarps * i;
                 if (e >= vecs) continue;
-                float t[8];
-                Vec8<float>::load(j + 8 * e, t);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) dg[i][q] += t[q];
-                Vec8<float>::load(j + cols + 8 * e, t);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) db[i][q] += t[q];
+                for (int q = 0; q < 4; ++q) {
+                    dg[i][q] = tc::fma2(*reinterpret_cast<const float2 *>(j + 8 * e + 2 * q), one, dg[i][q]);
+                    db[i][q] = tc::fma2(*reinterpret_cast<const float2 *>(j + cols + 8 * e + 2 * q), one, db[i][q]);
+                }
             }
         }
     }
@@ -363,8 +392,11 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
     for (int i = 0; i < kBwdVec; ++i) {
         const int e = v0 + 32 * kWarps * i;
         if (e < vecs) {
-            Vec8<float>::store(out + 8 * e, dg[i]);
-            Vec8<float>::store(out + cols + 8 * e, db[i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                *reinterpret_cast<float2 *>(out + 8 * e + 2 * q) = dg[i][q];
+                *reinterpret_cast<float2 *>(out + cols + 8 * e + 2 * q) = db[i][q];
+            }
         }
     }
 }
