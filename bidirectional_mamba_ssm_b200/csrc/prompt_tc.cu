@@ -211,8 +211,9 @@ prompt_prep_kernel(const PromptParams p)
             if (r.bad) record_error(p.status, kStatusBadSlot);
             int all, nseg, seg;
             const int at = chunks + block_scan(r.chunks, &all);
-            chunks += all;
-            if (r.ok && at + r.chunks > p.max_chunks) {   // ranges that overlap: more rows than there are
+            // (ranges that overlap may have any number of chunks together)
+            chunks = min(chunks + all, p.max_chunks + 1);
+            if (r.ok && at + r.chunks > p.max_chunks) {   // such ranges: more rows than there are
                 r.ok = false;
                 record_error(p.status, kStatusBadSlot);
             }
@@ -239,7 +240,7 @@ prompt_prep_kernel(const PromptParams p)
             Prompt r = read_prompt(p, s);
             int all, nseg, seg;
             const int at = chunks + block_scan(r.chunks, &all);
-            chunks += all;
+            chunks = min(chunks + all, p.max_chunks + 1);
             if (at + r.chunks > p.max_chunks) r.ok = false;
             shape(r, nseg, seg);
             const bool cut = r.ok && nseg > 1;
@@ -382,8 +383,10 @@ constexpr uint32_t kOffBh = kOffC + kTile;          // B hi [s][n]
 constexpr uint32_t kOffBl = kOffBh + kTile;         // B lo [s][n], then the bf16 copy of the state [p'][n]
 constexpr uint32_t kOffX0 = kOffBl + kTile;         // X^T [p'][s], then the finished rows: even chunks
 constexpr uint32_t kOffX1 = kOffX0 + kTile;         // odd chunks
-constexpr uint32_t kOffRaw = kOffX1 + kTile;        // raw x [131][128]
+constexpr uint32_t kOffRaw1 = kOffX1;               // raw x [131][128] of odd chunks (state-only walk: no X^T)
+constexpr uint32_t kOffRaw = kOffX1 + kTile + 1024; // of even ones (of all, in the other walk)
 constexpr uint32_t kRawBytes = kRawRows * kPP * 2;
+static_assert(kOffRaw1 + kRawBytes <= kOffRaw, "raw buffers");
 constexpr uint32_t kOffFac = kOffRaw + kRawBytes;   // per-slot factors, f32 [2 parity][2 head][128] each:
 constexpr uint32_t kFac = 2 * 2 * kQ * 4;
 constexpr int kParts = 5;                           // of a chunk's units: 3 x 4 (X group), 2 x 2 (M group)
@@ -551,7 +554,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     int *any_bad = reinterpret_cast<int *>(sm + kOffAnyBad);
     const uint32_t mb = sbase + kOffMbar;
     const uint32_t mb_bc = mb;            // [k] B/C tiles landed (state-only: even chunks, odd ones at mb_g)
-    const uint32_t mb_x = mb + 8;         // [k] raw x landed
+    const uint32_t mb_x = mb + 8;         // [k] raw x landed (state-only: even chunks, odd ones at mb_cs)
     const uint32_t mb_cs = mb + 16;       // [k] the copy of the state entering it ready
     const uint32_t mb_g = mb + 24;        // [k] G done
     const uint32_t mb_m = mb + 32;        // [k] M ready
@@ -575,9 +578,12 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     auto tokens = [&](int k) { return min(kQ, left - k * kQ); };
     auto first_row = [&](int k) { return row0 + k * kQ; };
 
+    // (the state-only walk has two raw buffers)
+    auto raw_off = [](int k) { return kStateOnly && (k & 1) ? kOffRaw1 : kOffRaw; };
+    auto x_bar = [&](int k) { return kStateOnly && (k & 1) ? mb_cs : mb_x; };
     auto issue_x = [&](int k) {
-        tc::mbar_expect_tx(mb_x, kRawBytes);
-        tc::tma_load_3d(sbase + kOffRaw, &tm_x, hp * kPP, first_row(k) - 3, 0, mb_x);
+        tc::mbar_expect_tx(x_bar(k), kRawBytes);
+        tc::tma_load_3d(sbase + raw_off(k), &tm_x, hp * kPP, first_row(k) - 3, 0, x_bar(k));
     };
     // B hi, B lo and C tiles of chunk k: three arrivals of mb_bc's phase (two
     // in the state-only walk, which has two B buffers: odd chunks in the C and
@@ -650,6 +656,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (!kStateOnly) issue_c(0);
         }
         if (kStateOnly && nk > 1) {
+            issue_x(1);
             issue_bh(1);
             issue_bl(1);
         }
@@ -673,7 +680,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int par = k & 1;
         const float4 w4 = taps[pr];
         const float bias = biases[pr];
-        const uint8_t *raw = sm + kOffRaw + 2 * pr;
+        const uint8_t *raw = sm + raw_off(k) + 2 * pr;
         auto ld = [&](int i) -> float {   // row i of the tile: token i - 3 of the chunk
             return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(raw + i * (kPP * 2))) << 16);
         };
@@ -771,7 +778,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (k > 1) ok = wait(ok, of(mb_xf0, k - 2), phase(k - 2));
             if (k > 0) ok = wait(ok, of(mb_sd0, k - 1), phase(k - 1));
         }
-        return wait(ok, mb_x, k & 1);
+        return wait(ok, x_bar(k), kStateOnly ? phase(k) : k & 1);
     };
 
     if (warp >= kProducerWarp) take_registers<kRegsOne>();
@@ -813,7 +820,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             take(mb_s, par);
             take(of(mb_w0, k), phase(k));
             if (!all_ok()) break;
-            if (issuer && k + 1 < nk) issue_x(k + 1);   // (the raw rows have been read)
+            constexpr int ahead = kStateOnly ? 2 : 1;
+            if (issuer && k + ahead < nk) issue_x(k + ahead);   // (the raw rows have been read)
             tc::fence_after_sync();
             if (issuer) {
                 const uint64_t dBh = tc::smem_desc(sbase + bh_off(k), kTile / 2, 1024);   // MN-major B
@@ -1001,12 +1009,11 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // that block (past it: zeros).
         // Between two Ms, while G is made: its share of the next chunk's conv.
         take_registers<kRegsM>();
-        {
-            const int h = warp >> 2, quad = warp & 3, row = tid & 127;
-            const uint32_t gcol = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kColG;
-            bool ok = true;
-            for (int k = -1; k < nk; ++k) {
-              if (!kStateOnly && k >= 0) {
+        const int h = warp >> 2, quad = warp & 3, row = tid & 127;
+        const uint32_t gcol = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kColG;
+        bool ok = true;
+        for (int k = -1; k < nk; ++k) {
+            if (!kStateOnly && k >= 0) {
                 const int par = k & 1;
                 ok = grp_and<kMGroup>(1, tid != 0 || wait(true, mb_g, par));
                 if (!ok) break;
@@ -1102,8 +1109,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::mbar_arrive(mb_m);
                     tc::mbar_arrive(of(mb_free0, k));
                 }
-              }
-              if (k + 1 < nk) {
+            }
+            if (k + 1 < nk) {
                 ok = grp_and<kMGroup>(1, tid != 0 || x_ready(k + 1));
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -1113,10 +1120,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::mbar_arrive(of(mb_w0, k + 1));
                     if (kStateOnly) tc::mbar_arrive(of(mb_free0, k + 1));
                 }
-              }
             }
-            if (!ok && tid == 0) record_error(p.status, kStatusTimeout);
         }
+        if (!ok && tid == 0) record_error(p.status, kStatusTimeout);
     } else if (warp < kXWarp) {
         // ================= Y group.  State: thread (p' = row, half of n), its
         // 64 values in registers.  Rows: thread (t = row, head).

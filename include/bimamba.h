@@ -366,8 +366,9 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
  *   xbc        : (len, ch) raw xBC, dtype;  dt : (len, H) dtype, positive
  *   A, D, conv_w (required), conv_b (nullable) : as above
  *   cu_seqlens : (batch + 1) int32, device -- prompt s is the rows
- *                cu_seqlens[s] .. cu_seqlens[s + 1] - 1; rows outside every
- *                prompt are not read and their y is left as it was
+ *                cu_seqlens[s] .. cu_seqlens[s + 1] - 1, and must not
+ *                decrease; rows outside every prompt do not matter and their
+ *                y is left as it was
  *   state_pool : (pool_size, H, P, N) fp32;  tail_pool : (pool_size, 4, ch)
  *                dtype -- prompt s's entry slots[s] gets its state after the
  *                last token and its last 4 raw tokens, in place
@@ -385,7 +386,10 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
  * range inside [0, len), is skipped (y and the pool untouched) and makes
  * bimamba_get_error report BIMAMBA_ERR_INVALID.  A negative slot marks a
  * padding entry of the batch: skipped without an error.
- * y must not overlap an input or the pool.
+ * An infinity or NaN among a prompt's inputs reaches its own rows from that
+ * token on (the heads and channels that it enters) and its entry, no others.
+ * y must not overlap an input or the pool.  len up to 2^30 (else
+ * BIMAMBA_ERR_UNSUPPORTED).
  */
 size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d);
 

@@ -349,3 +349,17 @@ def test_larger_batch_of_the_model_shape(lib):
     for k in range(len(lens)):
         assert ref.far(s[k], to_np(fs[k])) <= 2 * STATE_TOL
     assert torch.equal(t.float(), ft)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_ranges_of_the_same_rows(lib, dtype):
+    """Prompts that all name the same 1280 rows (their ranges run backwards in
+    between) are more than a call of that many rows can hold: reported, every
+    entry of the pool finite, and the next call right."""
+    shape, n, rows = (2, 64, 128), 64, 1280
+    d = ref.draw(rows, n, *shape, dtype, seed=8, pool=n)
+    y, s, t = ref.run(lib, d, [0] * n, [1] * n, *shape, cu=[0, rows] * (n // 2) + [0])
+    assert lib.bimamba_get_error() == lib.BIMAMBA_ERR_INVALID
+    assert torch.isfinite(s).all() and torch.isfinite(t).all()
+    d = ref.draw(100, 1, *shape, dtype, seed=9, pool=2)
+    _check(lib, d, [100], [1], shape)
