@@ -9,6 +9,7 @@ cannot be loaded, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -160,12 +161,16 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _code_of(dtype) -> int:
+    if dtype == torch.float32:
         return BIMAMBA_F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return BIMAMBA_BF16
-    raise BimambaError(BIMAMBA_ERR_UNSUPPORTED, f"dtype {t.dtype}")
+    raise BimambaError(BIMAMBA_ERR_UNSUPPORTED, f"dtype {dtype}")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _code_of(t.dtype)
 
 
 def _check(status: int, where: str):
@@ -385,35 +390,33 @@ def bimamba_out_proj(y, w_out, out, stream=None):
     return out
 
 
-def _call(where, fn, stream, lead, before, specs, after):
-    """fn(*before, pointers of specs, *after, stream).  A spec is (name,
-    tensor or None, dtype, shape), a dense CUDA tensor on lead's device; a
-    number stands for itself.  That device is made current
-    for the call: the kernels launch there, on its current stream unless one
-    is given."""
-    index = lead.get_device()
+def _call(where, fn, stream, before, specs, args, after):
+    """fn(*before, args, *after, stream) with each tensor's pointer in its
+    place.  A tensor's spec is (name, dtype, shape), dense on the first one's
+    CUDA device (or None itself); where the spec is None the argument stands
+    for itself.  That device is made current for the call: the kernels launch
+    there, on its current stream unless one is given."""
+    index = args[0].get_device()
     if index < 0:
-        raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: a CUDA tensor is wanted, got one on {lead.device}")
-    args = list(before)
-    for spec in specs:
-        if spec.__class__ is not tuple:
-            args.append(spec)
+        raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: a CUDA tensor is wanted, got one on {args[0].device}")
+    out = []
+    for spec, t in zip(specs, args):
+        if t is None or spec is None:
+            out.append(t)
             continue
-        name, t, dtype, shape = spec
-        if t is None:
-            args.append(None)
-            continue
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        if t.dtype is not spec[1] or t.shape != spec[2] or t.get_device() != index or not t.is_contiguous():
+            name, dtype, shape = spec
             raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: {name}: a dense {dtype} tensor of shape {tuple(shape)} "
-                               f"on {lead.device} is wanted, got {t.dtype} {tuple(t.shape)} with strides "
+                               f"on {args[0].device} is wanted, got {t.dtype} {tuple(t.shape)} with strides "
                                f"{t.stride()} on {t.device}")
-        args.append(t.data_ptr())
-    args.extend(after)
+        out.append(t.data_ptr())
+    # (the raw handle: a Stream object takes 3 us to make, a fifth of a call)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
     if torch.cuda.current_device() == index:
-        st = fn(*args, _stream(stream))
+        st = fn(*before, *out, *after, handle)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, _stream(stream))
+            st = fn(*before, *out, *after, handle)
     if st != BIMAMBA_OK:
         raise BimambaError(st, where)
 
@@ -427,17 +430,38 @@ def _workspace(where, t, lead):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _causal_inputs(xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state):
-    """The inputs that the prompt scan and the token step share."""
-    rows, f32, td, ch = xbc.shape[0], torch.float32, xbc.dtype, heads * headdim + 2 * d_state
-    return (("xbc", xbc, td, (rows, ch)), ("dt", dt, td, (rows, heads)), ("A", A, f32, (heads,)),
-            ("D", D, f32, (heads,)), ("conv_w", conv_w, f32, (ch, 4)), ("conv_b", conv_b, f32, (ch,)))
+# What a call's sizes alone decide is made once for them (a few microseconds,
+# where a short call takes some fifteen).
+@functools.lru_cache(maxsize=1024)
+def _causal_specs(td, rows, prompts, pool, heads, headdim, d_state):
+    """(dims, specs) of the prompt scan, and with prompts None of the token step."""
+    f32, i32, inner, ch = torch.float32, torch.int32, heads * headdim, heads * headdim + 2 * d_state
+    step = prompts is None
+    dims = make_dims(rows if step else prompts, 1 if step else rows, heads, headdim, d_state, _code_of(td))
+    n = rows if step else prompts
+    specs = [("xbc", td, (rows, ch)), ("dt", td, (rows, heads)), ("A", f32, (heads,)), ("D", f32, (heads,)),
+             ("conv_w", f32, (ch, 4)), ("conv_b", f32, (ch,)), ("cu_seqlens", i32, (n + 1,)),
+             ("state_pool", f32, (pool, heads, headdim, d_state)), ("tail_pool", td, (pool, 4, ch)), None,
+             ("slots", i32, (n,)), ("resume", i32, (n,)), ("y", td, (rows, inner))]
+    if step:
+        specs = [v for v in specs if v is None or v[0] not in ("cu_seqlens", "resume")]
+    return (ctypes.byref(dims),), tuple(specs)
 
 
-def _causal_pool(state_pool, tail_pool, dtype, heads, headdim, d_state):
-    pool = state_pool.shape[0]
-    return (("state_pool", state_pool, torch.float32, (pool, heads, headdim, d_state)),
-            ("tail_pool", tail_pool, dtype, (pool, 4, heads * headdim + 2 * d_state)), pool)
+@functools.lru_cache(maxsize=1024)
+def _norm_specs(td, shape, backward):
+    """(dtype code, (rows, cols), specs) of the layer norm or its backward pass."""
+    if not shape:
+        raise BimambaError(BIMAMBA_ERR_INVALID, "layer norm of a tensor without dimensions")
+    f32, cols, each = torch.float32, shape[-1], shape[:-1]
+    vec, rows = (cols,), shape.numel() // cols if cols else 0
+    if backward:
+        specs = (("dy", td, shape), ("h", td, shape), ("gamma", f32, vec), ("mean", f32, each), ("rstd", f32, each),
+                 ("dsum", td, shape), ("dx", td, shape), ("dgamma", f32, vec), ("dbeta", f32, vec))
+    else:
+        specs = (("x", td, shape), ("residual", td, shape), ("gamma", f32, vec), ("beta", f32, vec), None,
+                 ("y", td, shape), ("sum_out", td, shape), ("mean", f32, each), ("rstd", f32, each))
+    return _code_of(td), (rows, cols), specs
 
 
 def bimamba_prompt_workspace_bytes(dims: Dims) -> int:
@@ -459,13 +483,10 @@ def bimamba_prompt_scan(xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, t
     pool entry slots[s] gets the prompt's state and last raw tokens, and is
     what it continues from where resume[s] != 0 (resume None: nowhere).
     cu_seqlens, slots and resume are int32 device tensors."""
-    td, n, i32 = xbc.dtype, slots.shape[0], torch.int32
-    dims = make_dims(n, xbc.shape[0], heads, headdim, d_state, _dtype_code(xbc))
-    _call("bimamba_prompt_scan", _lib.bimamba_prompt_scan, stream, xbc, (ctypes.byref(dims),),
-          (*_causal_inputs(xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state),
-           ("cu_seqlens", cu_seqlens, i32, (n + 1,)),
-           *_causal_pool(state_pool, tail_pool, td, heads, headdim, d_state), ("slots", slots, i32, (n,)),
-           ("resume", resume, i32, (n,)), ("y", y, td, (xbc.shape[0], heads * headdim))),
+    pool = state_pool.shape[0]
+    dims, specs = _causal_specs(xbc.dtype, xbc.shape[0], slots.shape[0], pool, heads, headdim, d_state)
+    _call("bimamba_prompt_scan", _lib.bimamba_prompt_scan, stream, dims, specs,
+          (xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, tail_pool, pool, slots, resume, y),
           _workspace("bimamba_prompt_scan", workspace, xbc))
     return y
 
@@ -485,12 +506,10 @@ def bimamba_token_step(xbc, dt, A, D, conv_w, conv_b, state_pool, tail_pool, slo
     """One new token of each of a batch of cached streams: row s of xbc
     (rows, ch) and dt (rows, H) continues from pool entry slots[s], which is
     updated in place, into row s of y (rows, H*P)."""
-    td, rows = xbc.dtype, xbc.shape[0]
-    dims = make_dims(rows, 1, heads, headdim, d_state, _dtype_code(xbc))
-    _call("bimamba_token_step", _lib.bimamba_token_step, stream, xbc, (ctypes.byref(dims),),
-          (*_causal_inputs(xbc, dt, A, D, conv_w, conv_b, heads, headdim, d_state),
-           *_causal_pool(state_pool, tail_pool, td, heads, headdim, d_state),
-           ("slots", slots, torch.int32, (rows,)), ("y", y, td, (rows, heads * headdim))),
+    pool = state_pool.shape[0]
+    dims, specs = _causal_specs(xbc.dtype, xbc.shape[0], None, pool, heads, headdim, d_state)
+    _call("bimamba_token_step", _lib.bimamba_token_step, stream, dims, specs,
+          (xbc, dt, A, D, conv_w, conv_b, state_pool, tail_pool, pool, slots, y),
           _workspace("bimamba_token_step", workspace, xbc))
     return y
 
@@ -500,15 +519,9 @@ def bimamba_layer_norm(x, gamma, beta, y, mean, rstd, *, residual=None, sum_out=
     """y = layer norm of x (+ residual) over the last dimension, gamma/beta
     (beta may be None) fp32; mean and rstd (one fp32 value a row) and, with a
     residual, sum_out = x + residual are written for the backward pass."""
-    td, shape, f32 = x.dtype, x.shape, torch.float32
-    cols, each = shape[-1], shape[:-1]
-    rows = x.numel() // cols if cols else 0
-    vec = (cols,)
-    _call(
-        "bimamba_layer_norm", _lib.bimamba_layer_norm, stream, x, (rows, cols),
-        (("x", x, td, shape), ("residual", residual, td, shape), ("gamma", gamma, f32, vec),
-         ("beta", beta, f32, vec), eps, ("y", y, td, shape), ("sum_out", sum_out, td, shape),
-         ("mean", mean, f32, each), ("rstd", rstd, f32, each)), (_dtype_code(x),))
+    code, sizes, specs = _norm_specs(x.dtype, x.shape, False)
+    _call("bimamba_layer_norm", _lib.bimamba_layer_norm, stream, sizes, specs,
+          (x, residual, gamma, beta, eps, y, sum_out, mean, rstd), (code,))
     return y
 
 
@@ -528,15 +541,10 @@ def bimamba_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dgamma, dbeta, wor
     """Gradients of the layer norm from dy (and dsum, the gradient that
     reaches h past the norm): writes dx, dgamma and, unless None, dbeta.
     h is the forward call's x, or its sum_out where it had a residual."""
-    td, shape, f32 = h.dtype, h.shape, torch.float32
-    cols, each = shape[-1], shape[:-1]
-    rows = h.numel() // cols if cols else 0
-    vec = (cols,)
-    _call("bimamba_layer_norm_backward", _lib.bimamba_layer_norm_backward, stream, h, (rows, cols),
-          (("dy", dy, td, shape), ("h", h, td, shape), ("gamma", gamma, f32, vec), ("mean", mean, f32, each),
-           ("rstd", rstd, f32, each), ("dsum", dsum, td, shape), ("dx", dx, td, shape),
-           ("dgamma", dgamma, f32, vec), ("dbeta", dbeta, f32, vec)),
-          (_dtype_code(h), *_workspace("bimamba_layer_norm_backward", workspace, h)))
+    code, sizes, specs = _norm_specs(h.dtype, h.shape, True)
+    _call("bimamba_layer_norm_backward", _lib.bimamba_layer_norm_backward, stream, sizes, specs,
+          (dy, h, gamma, mean, rstd, dsum, dx, dgamma, dbeta),
+          (code, *_workspace("bimamba_layer_norm_backward", workspace, h)))
     return dx
 
 
