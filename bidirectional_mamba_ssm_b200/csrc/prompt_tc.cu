@@ -66,8 +66,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // One walk: `chunks` chunks of prompt `seq` from chunk `chunk`, whose operand
 // rows start at chunk `act` of the operand array.
-struct Walk {
+struct __align__(16) Walk {
     int seq, chunk, chunks, act;
+    int begin, len;    // the prompt's rows
+    int entry;         // its pool entry
+    int resume;        // whether it continues from that
     int slot;          // entering state's slot (prompts in segments), or -1
     int last;          // the prompt's last segment
     int pad0, pad1;
@@ -259,10 +262,12 @@ prompt_prep_kernel(const PromptParams p)
             }
             if (s < p.batch) p.segs[s] = make_int2(slot, cut ? nseg : 1);
             if (!r.ok) continue;
+            const int entry = p.slots[s], resume = p.resume && p.resume[s] != 0;
             for (int i = 0; i < nseg - 1; ++i)
-                p.walks[wi + i] = Walk{s, i * seg, seg, at + i * seg, slot + i, 0, 0, 0};
+                p.walks[wi + i] = Walk{s, i * seg, seg, at + i * seg, r.begin, r.len, entry, resume, slot + i, 0, 0, 0};
             const int first = (nseg - 1) * seg;
-            p.walks[wl] = Walk{s, first, tail_chunks, at + first, cut ? slot + nseg - 1 : -1, 1, 0, 0};
+            p.walks[wl] = Walk{s,      first, tail_chunks, at + first, r.begin, r.len, entry,
+                               resume, cut ? slot + nseg - 1 : -1, 1, 0, 0};
         }
         return;
     }
@@ -402,6 +407,8 @@ constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of bo
 constexpr uint32_t kOffTaps = kOffDtBuf + 2 * kQ * 4;   // float4 [128] conv taps, float [128] biases, float [2] D, float [3][128] halo
 constexpr uint32_t kOffMbar = kOffTaps + kPP * 20 + 8 + 3 * kPP * 4;
 constexpr uint32_t kOffTmem = kOffMbar + 160;
+constexpr uint32_t kStateRow = kN * 4 + 16;         // a row of the last state on its way out: 16-byte stores of
+static_assert(kPP * kStateRow <= 3 * kTile, "state rows");   // 8 threads' rows meet no bank twice
 
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
 static_assert(kOffRaw % 1024 == 0 && kOffFac % 16 == 0 && kOffMbar % 8 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
@@ -527,11 +534,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // (a programmatic launch: everything read below was written by kernels
     // before this one)
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Walk wk = p.walks[wi];   // (requested beside the table's length: the table has an entry for every CTA)
     if (wi >= (kStateOnly ? p.head->inner : p.head->total)) return;
-    const Walk wk = p.walks[wi];
-    const int slot = p.slots[wk.seq];
-    const int begin = p.cu[wk.seq], len = p.cu[wk.seq + 1] - begin;
-    const bool resume = p.resume && p.resume[wk.seq] != 0;
+    const int slot = wk.entry, begin = wk.begin, len = wk.len;
+    const bool resume = wk.resume != 0;
     const int nk = wk.chunks;
     __nv_bfloat16 *tail = p.tail + (size_t)slot * 4 * ch;
     if constexpr (!kStateOnly) {
@@ -661,7 +667,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             issue_bl(1);
         }
     }
+    float A0 = 0.0f, A1 = 0.0f;
     if (warp == kHelperWarp) {
+        A0 = p.A[2 * hp] * kLog2e;
+        A1 = p.A[2 * hp + 1] * kLog2e;
         if (nk > 0) load_dt_async(0);
         if (nk > 1) load_dt_async(1);
     }
@@ -901,7 +910,6 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         __syncwarp();
     } else if (warp == kHelperWarp) {
         bool ok = true;
-        const float A0 = p.A[2 * hp] * kLog2e, A1 = p.A[2 * hp + 1] * kLog2e;
         for (int k = 0; k < nk; ++k) {
             const int b = k & 1;
             if (k >= 2) {
@@ -912,7 +920,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
             const __nv_bfloat162 *src = reinterpret_cast<const __nv_bfloat162 *>(sm + kOffDtBuf) + b * kQ + 4 * lane;
-#pragma unroll 1
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // slots 4 lane .. 4 lane + 3: prefix sums c and, for w, suffix
                 // sums c_last - c (from the end, so that the factors that
@@ -952,8 +960,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     scl[b * 2 + h] = make_float2(all > -1.0f ? expm1f(all * kLn2) : exp2f(all), all);
             }
             __syncwarp();
-#pragma unroll 1
-            for (int e = b * 2 * kQ + lane; e < (b + 1) * 2 * kQ; e += 32) {   // [parity][head][slot]
+#pragma unroll 4
+            for (int i = 0; i < 2 * kQ / 32; ++i) {   // [parity][head][slot]
+                const int e = b * 2 * kQ + 32 * i + lane;
                 const float c = cum[e], d = dts[e];
                 wgt[e] = tc::exp2_approx(wgt[e]) * d;
                 if constexpr (!kStateOnly) {
@@ -1278,17 +1287,28 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // entry).  Its place is looked up again: not a register is spared for
         // it through the loop.
         const Walk end = p.walks[blockIdx.x / HP];
-        const bool again = p.resume && p.resume[end.seq] != 0;
-        if (ok && (kStateOnly || end.last) && (nk > 0 || !again)) {
-            const size_t off = (size_t)hp * kPP * kN + (size_t)prow * kN + 64 * hf;
-            float *to = kStateOnly ? p.seg_state + (size_t)(end.slot + 1) * H * kP * kN + off
-                                   : p.state + (size_t)p.slots[end.seq] * H * kP * kN + off;
+        if (ok && (kStateOnly || end.last) && (nk > 0 || !end.resume)) {
+            // through the B and C tiles, which nothing reads or loads any
+            // more, and 512-byte copies (a thread's own 16-byte stores, 512
+            // bytes apart in a warp, took 4 us)
+            uint8_t *rows = sm + kOffC + prow * kStateRow;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                *reinterpret_cast<float4 *>(to + 4 * i) =
+                *reinterpret_cast<float4 *>(rows + 256 * hf + 16 * i) =
                     make_float4(st[2 * i].x, st[2 * i].y, st[2 * i + 1].x, st[2 * i + 1].y);
-            if (kStateOnly && hf == 0 && (prow & 63) == 0)
-                p.seg_dec[(size_t)(end.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
+            tc::fence_proxy_async();
+            grp_sync<kYGroup>(2);
+            if (hf == 0) {
+                float *to = (kStateOnly ? p.seg_state + (size_t)(end.slot + 1) * H * kP * kN
+                                        : p.state + (size_t)end.entry * H * kP * kN) +
+                            (size_t)hp * kPP * kN + (size_t)prow * kN;
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                             ::"l"(to), "r"(tc::smem_u32(rows)), "n"(kN * 4) : "memory");
+                tc::bulk_commit();
+                tc::bulk_wait0();
+                if (kStateOnly && (prow & 63) == 0)
+                    p.seg_dec[(size_t)(end.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
+            }
         }
         if (!ok && tb == 0) record_error(p.status, kStatusTimeout);
     } else if (warp < kProducerWarp) {
@@ -1318,10 +1338,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // the new tail: by the prompt's first walk (the only one that read the
         // old x channels; the old B and C channels were read by the prep kernel)
         if (starts) {
-            const int seq = p.walks[blockIdx.x / HP].seq;
-            const bool again = p.resume && p.resume[seq] != 0;
-            const int from = p.cu[seq], n = p.cu[seq + 1] - from;
-            __nv_bfloat16 *entry = p.tail + (size_t)p.slots[seq] * 4 * ch;
+            const Walk end = p.walks[blockIdx.x / HP];
+            const bool again = end.resume != 0;
+            const int from = end.begin, n = end.len;
+            __nv_bfloat16 *entry = p.tail + (size_t)end.entry * 4 * ch;
             auto commit = [&](int cc) {
                 __nv_bfloat16 v[4];
 #pragma unroll
@@ -1354,26 +1374,28 @@ struct Layout {
     size_t head, walks, segs, act, dec, state, bytes;
 };
 
-// How prompts are cut.  A prompt is cut once its walk would take a fifth
-// longer than the GPU's average share of the call (cut_over chunks; never
-// below 4).  The pieces are as long as is best for one prompt of all the
-// rows: n pieces take ceil(n pairs / SMs) rounds of a piece's chunks, after
-// state-only walks of the first n - 1 at about half the time a chunk.
+// How prompts are cut.  The pieces are as long as is best for one prompt of
+// all the rows: n pieces take ceil(n pairs / SMs) rounds of a piece's chunks
+// and about 3 chunks' time to begin and end, after state-only walks of the
+// first n - 1 at half of that.  A prompt is cut once its walk would take
+// longer than these do: a piece's state-only walk, three chunks' time for two
+// more launches, and the GPU's share of the call (a fifth added: walks do not
+// fill it evenly).  1311, 1, 640, 129, 0, 2777, 63, 1024, 517, 1536 and 128
+// tokens in 64 heads: 150 us; with the 2777 in two pieces, 178.
 void cut_of(long long chunks, int pairs, int &cut_over, int &seg_chunks)
 {
     const long long share = (chunks * pairs + kSMs - 1) / kSMs;
-    cut_over = (int)std::max<long long>(4, (share * 6 + 4) / 5);
-    long long best = 1ll << 60;
-    seg_chunks = cut_over;
+    long long best = 1ll << 60, piece = chunks;
     for (long long n = 2; n <= 16 && n <= chunks; ++n) {
         const long long seg = (chunks + n - 1) / n;
-        const long long cost = seg * (2 * ((n * pairs + kSMs - 1) / kSMs) + ((n - 1) * pairs + kSMs - 1) / kSMs);
+        const long long cost = (seg + 3) * (2 * ((n * pairs + kSMs - 1) / kSMs) + ((n - 1) * pairs + kSMs - 1) / kSMs);
         if (cost < best) {
             best = cost;
-            seg_chunks = (int)seg;
+            piece = seg;
         }
     }
-    seg_chunks = std::min(seg_chunks, cut_over);
+    cut_over = (int)(std::max(piece, (share * 6 + 4) / 5) + piece / 2 + 3);
+    seg_chunks = (int)std::max<long long>(1, std::min<long long>(piece, cut_over));
 }
 
 // Sizes that hold for any lengths of `batch` prompts in `len` rows: a prompt
