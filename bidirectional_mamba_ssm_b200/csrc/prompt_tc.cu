@@ -419,10 +419,10 @@ constexpr uint32_t kColY = 128;    // Y, 64 columns per head
 constexpr uint32_t kColW = 256;    // (w o X)^T, A operand: 64 columns hi, 64 columns lo
 constexpr uint32_t kColS = 384;    // a chunk's (w o X)^T B [p' = lane][n], fp32
 
-// ---- warps: groups of 8, 8 and 12 and single ones (one of 4 is idle: the
-// register shares below are given to whole sets of 4 warps)
+// ---- warps: groups of 8, 8 and 12 and 4 single ones (the register shares
+// below are given to whole sets of 4 warps)
 constexpr int kMGroup = 256, kYGroup = 256, kXGroup = 384;   // threads
-constexpr int kYWarp = 8, kXWarp = 16, kProducerWarp = 28, kHelperWarp = 29, kPublisherWarp = 30;
+constexpr int kYWarp = 8, kXWarp = 16, kProducerWarp = 28, kHelperWarp = 29, kPublisherWarp = 30, kTailWarp = 31;
 constexpr int kThreads = 32 * 32;
 // registers a thread: 1024 threads are launched with 64; the Y group holds
 // the state (64 values a thread)
@@ -517,6 +517,8 @@ template <int kCount> __device__ __forceinline__ bool grp_and(int id, bool pred)
 //   warp 28      producer: every MMA, the B/C tile loads.
 //   warp 29      helper: dt copies, prefix sums and factors, two chunks ahead.
 //   warp 30      publisher: finished rows to y.
+//   warp 31      the new tail of the prompt's entry (behind the others' loops
+//                in the code: there it costs them no registers).
 template <bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_bc,
@@ -531,25 +533,6 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int H = p.H, ch = p.ch, HP = H / 2;
     const int hp = blockIdx.x % HP;
     const int wi = blockIdx.x / HP;
-    // (a programmatic launch: everything read below was written by kernels
-    // before this one)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Walk wk = p.walks[wi];   // (requested beside the table's length: the table has an entry for every CTA)
-    if (wi >= (kStateOnly ? p.head->inner : p.head->total)) return;
-    const int slot = wk.entry, begin = wk.begin, len = wk.len;
-    const bool resume = wk.resume != 0;
-    const int nk = wk.chunks;
-    __nv_bfloat16 *tail = p.tail + (size_t)slot * 4 * ch;
-    if constexpr (!kStateOnly) {
-        // an entry that two prompts name belongs to neither
-        bool twice = false;
-        for (int r = tid; r < p.batch; r += kThreads) twice |= r != wk.seq && p.slots[r] == slot;
-        if (__syncthreads_or(twice)) {
-            if (hp == 0 && wk.last && tid == 0) record_error(p.status, kStatusBadSlot);
-            return;
-        }
-    }
-
     float *cum = reinterpret_cast<float *>(sm + kOffCum);
     float *dts = reinterpret_cast<float *>(sm + kOffDt);
     float *fB = reinterpret_cast<float *>(sm + kOffFB);
@@ -579,6 +562,44 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     auto of = [](uint32_t pair, int k) { return pair + 8 * (k & 1); };
     auto phase = [](int k) -> uint32_t { return (k >> 1) & 1; };   // of a pair's barrier
     auto xbuf = [](int k) { return (k & 1) ? kOffX1 : kOffX0; };
+    // ---- set-up: first what no kernel before this one has written (a
+    // programmatic launch: this may run beside the end of that one)
+    float4 *taps = reinterpret_cast<float4 *>(sm + kOffTaps);
+    float *biases = reinterpret_cast<float *>(sm + kOffTaps + kPP * 16);   // then D of both heads
+    float4 my_taps = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float my_bias = 0.0f, A0 = 0.0f, A1 = 0.0f;
+    if (tid < kPP) {
+        my_taps = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + tid) * 4);
+        my_bias = p.conv_b ? p.conv_b[hp * kPP + tid] : 0.0f;
+    }
+    if (warp == kHelperWarp) {
+        A0 = p.A[2 * hp] * kLog2e;
+        A1 = p.A[2 * hp + 1] * kLog2e;
+    }
+    if (tid == 32 * kProducerWarp) {
+        tc::prefetch_tmap(&tm_x);
+        tc::prefetch_tmap(&tm_bc);
+        if (!kStateOnly) tc::prefetch_tmap(&tm_y);
+        tc::mbar_init(mb_bc, kStateOnly ? 2 : 3);
+        tc::mbar_init(mb_g, kStateOnly ? 2 : 1);
+        for (uint32_t b = mb_x; b < mb_dt0; b += 8)
+            if (b != mb_g && b != mb_w0 && b != mb_w0 + 8) tc::mbar_init(b, 1);
+        tc::mbar_init(mb_w0, 2);       // the X and the M group
+        tc::mbar_init(mb_w0 + 8, 2);
+        tc::mbar_init(mb_xf0, 1);
+        tc::mbar_init(mb_xf0 + 8, 1);
+        tc::mbar_init(mb_dt0, 32);
+        tc::mbar_init(mb_dt0 + 8, 32);
+        tc::mbar_init(mb_free0, 3);
+        tc::mbar_init(mb_free0 + 8, 3);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Walk wk = p.walks[wi];   // (requested beside the table's length: the table has an entry for every CTA)
+    if (wi >= (kStateOnly ? p.head->inner : p.head->total)) return;
+    const int slot = wk.entry, begin = wk.begin, len = wk.len;
+    const bool resume = wk.resume != 0;
+    const int nk = wk.chunks;
+    __nv_bfloat16 *tail = p.tail + (size_t)slot * 4 * ch;
     // chunk k's rows in the prompt
     const int left = len - wk.chunk * kQ, row0 = begin + wk.chunk * kQ;
     auto tokens = [&](int k) { return min(kQ, left - k * kQ); };
@@ -624,37 +645,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    // ---- set-up
-    float4 *taps = reinterpret_cast<float4 *>(sm + kOffTaps);
-    float *biases = reinterpret_cast<float *>(sm + kOffTaps + kPP * 16);   // then D of both heads
-    if (tid < kPP) {
-        taps[tid] = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(hp * kPP + tid) * 4);
-        biases[tid] = p.conv_b ? p.conv_b[hp * kPP + tid] : 0.0f;
-    }
-    if (tid < 2) biases[kPP + tid] = p.D[2 * hp + tid];
-    // the 3 tokens before the walk's first chunk where they are not in the raw
-    // tile: the prompt's entry's tail, or zeros
-    const bool starts = wk.chunk == 0;
-    float *halo = biases + kPP + 2;   // [3][128]
-    if (starts && tid < 3 * kPP)
-        halo[tid] = resume ? __bfloat162float(tail[(1 + tid / kPP) * ch + hp * kPP + tid % kPP]) : 0.0f;
-    if (warp == 0) tc::tmem_alloc(sbase + kOffTmem, 512);
     if (tid == 32 * kProducerWarp) {
-        tc::prefetch_tmap(&tm_x);
-        tc::prefetch_tmap(&tm_bc);
-        if (!kStateOnly) tc::prefetch_tmap(&tm_y);
-        tc::mbar_init(mb_bc, kStateOnly ? 2 : 3);
-        tc::mbar_init(mb_g, kStateOnly ? 2 : 1);
-        for (uint32_t b = mb_x; b < mb_dt0; b += 8)
-            if (b != mb_g && b != mb_w0 && b != mb_w0 + 8) tc::mbar_init(b, 1);
-        tc::mbar_init(mb_w0, 2);       // the X and the M group
-        tc::mbar_init(mb_w0 + 8, 2);
-        tc::mbar_init(mb_xf0, 1);
-        tc::mbar_init(mb_xf0 + 8, 1);
-        tc::mbar_init(mb_dt0, 32);
-        tc::mbar_init(mb_dt0 + 8, 32);
-        tc::mbar_init(mb_free0, 3);
-        tc::mbar_init(mb_free0 + 8, 3);
         if (nk > 0) {
             issue_x(0);
             issue_bh(0);
@@ -667,17 +658,41 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             issue_bl(1);
         }
     }
-    float A0 = 0.0f, A1 = 0.0f;
     if (warp == kHelperWarp) {
-        A0 = p.A[2 * hp] * kLog2e;
-        A1 = p.A[2 * hp + 1] * kLog2e;
         if (nk > 0) load_dt_async(0);
         if (nk > 1) load_dt_async(1);
     }
+    if (warp == 0) tc::tmem_alloc(sbase + kOffTmem, 512);
+    if (tid < kPP) {
+        taps[tid] = my_taps;
+        biases[tid] = my_bias;
+    }
+    if (tid < 2) biases[kPP + tid] = p.D[2 * hp + tid];
+    // the 3 tokens before the walk's first chunk where they are not in the raw
+    // tile: the prompt's entry's tail, or zeros
+    const bool starts = wk.chunk == 0;
+    float *halo = biases + kPP + 2;   // [3][128]
+    if (starts && tid < 3 * kPP)
+        halo[tid] = resume ? __bfloat162float(tail[(1 + tid / kPP) * ch + hp * kPP + tid % kPP]) : 0.0f;
+    // an entry that two prompts name belongs to neither
+    bool twice = false;
+    if (!kStateOnly)
+        for (int r = tid; r < p.batch; r += kThreads) twice |= r != wk.seq && p.slots[r] == slot;
     tc::fence_before_sync();
-    __syncthreads();
+    twice = __syncthreads_or(twice);
     tc::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + kOffTmem);
+    if (!kStateOnly && twice) {
+        // (the copies on their way land first)
+        if (tid == 32 * kProducerWarp) {
+            if (nk > 0 && !(mbar_wait(mb_x, 0) && mbar_wait(mb_bc, 0))) record_error(p.status, kStatusTimeout);
+            if (hp == 0 && wk.last) record_error(p.status, kStatusBadSlot);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        if (warp == 0) tc::tmem_dealloc(tmem, 512);
+        return;
+    }
 
     // conv + SiLU of channel p' = pr, units ua .. ub - 1 (8 tokens each) of
     // chunk k: X^T to shared memory, both halves of (w o X)^T to tensor
@@ -1305,7 +1320,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
                              ::"l"(to), "r"(tc::smem_u32(rows)), "n"(kN * 4) : "memory");
                 tc::bulk_commit();
-                tc::bulk_wait0();
+                tc::bulk_wait_read0();   // (shared memory must outlive the reads; the grid's end the writes)
                 if (kStateOnly && (prow & 63) == 0)
                     p.seg_dec[(size_t)(end.slot + 1) * H + 2 * hp + (prow >> 6)] = dec;
             }
@@ -1331,13 +1346,11 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
         if (!ok && tx == 0) record_error(p.status, kStatusTimeout);
     }
-    tc::fence_before_sync();
-    __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
     if constexpr (!kStateOnly) {
         // the new tail: by the prompt's first walk (the only one that read the
-        // old x channels; the old B and C channels were read by the prep kernel)
-        if (starts) {
+        // old x channels, in its set-up; the old B and C channels were read by
+        // the prep kernel)
+        if (starts && warp == kTailWarp) {
             const Walk end = p.walks[blockIdx.x / HP];
             const bool again = end.resume != 0;
             const int from = end.begin, n = end.len;
@@ -1353,10 +1366,13 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 4; ++i) entry[(size_t)i * ch + cc] = v[i];
             };
-            if (tid < kPP) commit(hp * kPP + tid);
-            else if (hp == 0 && tid < kPP + 2 * kN) commit(H * kP + tid - kPP);
+#pragma unroll 1
+            for (int i = lane; i < kPP + (hp == 0 ? 2 * kN : 0); i += 32) commit(i < kPP ? hp * kPP + i : H * kP + i - kPP);
         }
     }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
 bool prompt_tc_supported(const bimamba_dims &d)
