@@ -8,15 +8,20 @@
 //     u_t = SiLU(bias + sum_j w_j raw_{t-3+j})        (x, B and C channels)
 //     h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t^T,   y_t = h_t C_t + D x_t
 //
-// Bound by FP32 issue: 5 P N flops per token and head.  Two kernels:
+// Bound by FP32 issue: 5 P N flops per token and head.  1842 tokens in four
+// prompts (1024, 517, 1 and 300), 64 heads of 64 x 128: 305 us, where the
+// flops take 65; the longest prompt alone takes 183 (a warp's 16 fused
+// operations a row and token are half of its cycles, the rest latencies).
+// Two kernels:
 //   1. every channel activated, and each head's dt and decays, in fp32: what
-//      the walks read.  (Done inside the walks, by a warp beside two that
-//      compute, the conv and its exponentials bound them: 370 us instead of
-//      the time below.)
+//      the walks read.  30 us of the above.  (Done inside the walks, by a warp
+//      beside two that compute, the conv and its exponentials bound them: 370
+//      us in all.)
 //   2. one CTA per (prompt, head, slice of state rows): the rows of a state
 //      are independent, so a head's 64 rows are walked by several CTAs and a
 //      few prompts still fill the SMs.  A thread holds 4 rows x 8 columns in
-//      registers; the dot products with C over the kLpr threads of a row are
+//      registers (2 rows: 285 us above, but 16 prompts of 100 tokens 250 us
+//      for 180); the dot products with C over the kLpr threads of a row are
 //      summed for 4 tokens at a time by a transposing reduction (each shuffle
 //      halves the number of values: 15 shuffles for 16 sums, not 64).  The
 //      next 16 tokens come by asynchronous copies.

@@ -16,6 +16,8 @@
 // head's x and the row's B and C (recomputed by every head: they are small,
 // and a launch of their own would cost more than the reads) runs under those
 // loads.
+// 64 heads of 64 x 128: 256 rows fp32 184 us (bytes 170), 32 rows bf16 25
+// (21), one row 13, the host's call.
 #include "common.cuh"
 #include "dispatch.h"
 
@@ -26,7 +28,7 @@ namespace {
 constexpr int kStepThreads = 256;
 // 16-byte state loads a thread keeps in flight, and CTAs per SM.  256 rows of
 // 64 heads x 64 x 128: 8 loads and 3 CTAs 210 us, 8 and 4 195 us, 4 and 5
-// 182 us (the bytes take 170 us).
+// 182 us.
 constexpr int kStepLoads = 4, kStepCtas = 5;
 
 }  // namespace
