@@ -33,7 +33,8 @@
 // Kernels of one call:
 //   1. plan + conv of B and C: per 128-token chunk the operand rows
 //      [B hi | B lo | C] (zeros behind the prompt's end, so that a neighbour
-//      never enters a product), and, by one CTA, the table of walks.
+//      never enters a product), and, by one CTA, the table of walks.  All of
+//      it latency (7 us for 68 chunks of 11 prompts): short loops, few scans.
 //   2. only where a prompt may be long against the GPU's share of the work
 //      (segment_chunks): prompts above that are cut into equal segments; a
 //      state-only walk of each segment but the last, then
@@ -51,8 +52,8 @@
 // of G or M X, or freeing (w o X)^T a quarter at a time, gains nothing: the
 // conv, M and the row work then wait for the same issue slots.  A walk's
 // beginning and end take about 13 us besides.
-// Measured, 64 heads: 8 prompts of 4096 tokens 350 us, one of 32768 508, 11
-// ragged ones of 8137 in all 140, 37 tokens 26 (18 of them the host's call).
+// Measured, 64 heads: 8 prompts of 4096 tokens 350 us, one of 32768 505, 11
+// ragged ones of 8126 in all 133, 37 tokens 25 (18 of them the host's call).
 #include "common.cuh"
 #include "dispatch.h"
 #include "tc_ptx.cuh"
@@ -86,7 +87,8 @@ struct __align__(16) Walk {
 
 struct PlanHeader {
     int inner, total;  // walks that are not their prompt's last; all walks
-    int pad0, pad1;
+    int cuts;          // prompts in segments
+    int pad;
 };
 
 struct PromptParams {
@@ -98,7 +100,7 @@ struct PromptParams {
     __nv_bfloat16 *y, *act;
     PlanHeader *head;
     Walk *walks;
-    int2 *segs;              // per prompt: first slot, segments (1: whole)
+    int4 *cuts;              // per prompt in segments: prompt, first slot, segments
     float *seg_state;        // [slot][H][kP][kN]
     float *seg_dec;          // [slot][H], log2 of the segment's decay before it
     int *status;
@@ -130,23 +132,23 @@ __device__ __forceinline__ Prompt read_prompt(const PromptParams &p, int s)
     return r;
 }
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 512, kPrepCtas = 2;   // CTAs per chunk
 
 // Exclusive prefix sum over the CTA's threads, and the total.
-__device__ __forceinline__ int block_scan(int v, int *total)
+template <typename T> __device__ __forceinline__ T block_scan(T v, T *total)
 {
-    __shared__ int part[kPrepThreads / 32];
+    __shared__ T part[kPrepThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int run = v;
+    T run = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, run, o);
+        const T t = __shfl_up_sync(0xffffffffu, run, o);
         if (lane >= o) run += t;
     }
     __syncthreads();
     if (lane == 31) part[warp] = run;
     __syncthreads();
-    int before = 0, all = 0;
+    T before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kPrepThreads / 32; ++w) {
         if (w < warp) before += part[w];
@@ -195,15 +197,15 @@ __device__ __forceinline__ void tmem_st4_nw(uint32_t taddr, const uint32_t *r)
 
 }  // namespace
 
-// Plan (the last CTA) and B/C operand rows (one CTA per chunk of the operand
-// array).  A thread convolves 8 channels of 16 tokens.
+// Plan (the last CTA) and B/C operand rows (two CTAs per chunk of the operand
+// array).  A thread convolves 4 channels of 8 tokens.
 __global__ void __launch_bounds__(kPrepThreads)
 prompt_prep_kernel(const PromptParams p)
 {
     // the walk kernel behind this one may start its set-up
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
-    const int me = blockIdx.x;
+    const int me = blockIdx.x / kPrepCtas;
     if (me == p.max_chunks) {
         // ---- the table of walks.  First the walks that are not a prompt's
         // last segment (the state-only walks take exactly these), then the
@@ -232,19 +234,18 @@ prompt_prep_kernel(const PromptParams p)
             block_scan(r.ok ? nseg - 1 : 0, &all);
             inner += all;
             const int c = class_of(r.chunks - (nseg - 1) * seg);
+            unsigned long long four;   // 16 bits each
+            block_scan(r.ok ? 1ull << 16 * c : 0ull, &four);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                block_scan(r.ok && c == q, &all);
-                cls[q] += all;
-            }
+            for (int q = 0; q < 4; ++q) cls[q] += (int)(four >> 16 * q & 0xffffu);
         }
         int next[4];   // first walk of each class
         next[3] = inner;
         next[2] = next[3] + cls[3];
         next[1] = next[2] + cls[2];
         next[0] = next[1] + cls[1];
-        if (tid == 0) *p.head = PlanHeader{inner, next[0] + cls[0], 0, 0};
-        int inner_at = 0, slot_at = 0;
+        int inner_at = 0, cut_at = 0;
+        const int walks = next[0] + cls[0];
         chunks = 0;
         for (int s0 = 0; s0 < p.batch; s0 += kPrepThreads) {
             const int s = s0 + tid;
@@ -257,18 +258,20 @@ prompt_prep_kernel(const PromptParams p)
             const bool cut = r.ok && nseg > 1;
             const int wi = inner_at + block_scan(cut ? nseg - 1 : 0, &all);
             inner_at += all;
-            const int slot = slot_at + block_scan(cut ? nseg : 0, &all);
-            slot_at += all;
+            const int ci = cut_at + block_scan((int)cut, &all);
+            cut_at += all;
+            const int slot = wi + ci;   // (a cut prompt has a slot more than inner walks)
             const int tail_chunks = r.chunks - (nseg - 1) * seg;
             const int c = class_of(tail_chunks);
-            int wl = 0;
+            unsigned long long four;
+            const unsigned long long before = block_scan(r.ok ? 1ull << 16 * c : 0ull, &four);
+            int wl = (int)(before >> 16 * c & 0xffffu);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int at_q = next[q] + block_scan(r.ok && c == q, &all);
-                next[q] += all;
-                if (c == q) wl = at_q;
+                if (c == q) wl += next[q];
+                next[q] += (int)(four >> 16 * q & 0xffffu);
             }
-            if (s < p.batch) p.segs[s] = make_int2(slot, cut ? nseg : 1);
+            if (cut) p.cuts[ci] = make_int4(s, slot, nseg, 0);
             if (!r.ok) continue;
             const int entry = p.slots[s], resume = p.resume && p.resume[s] != 0;
             for (int i = 0; i < nseg - 1; ++i)
@@ -277,6 +280,7 @@ prompt_prep_kernel(const PromptParams p)
             p.walks[wl] = Walk{s,      first, tail_chunks, at + first, r.begin, r.len, entry,
                                resume, cut ? slot + nseg - 1 : -1, 1, 0, 0};
         }
+        if (tid == 0) *p.head = PlanHeader{inner, walks, cut_at, 0};
         return;
     }
 
@@ -295,64 +299,54 @@ prompt_prep_kernel(const PromptParams p)
     __syncthreads();
     const int4 f = found;
     if (f.x < 0) return;
-    const int g = tid & 31, sub = tid >> 5;
-    const int n0 = 8 * g;                      // channels n0 .. n0 + 7 of [B | C]
+    const int n0 = 4 * (tid & 63);             // channels n0 .. n0 + 3 of [B | C]
     const int c = p.H * kP + n0;
-    const int t0 = f.y * kQ + sub * 16;        // first token of this thread in the prompt
+    const int i0 = (blockIdx.x % kPrepCtas) * (kQ / kPrepCtas) + 8 * (tid >> 6);   // first token of this thread
+    const int t0 = f.y * kQ + i0;              // in the chunk and in the prompt
     const __nv_bfloat16 *raw = p.xbc + (size_t)f.z * p.ch + c;
     const bool resume = p.resume && p.resume[f.x] != 0;
     const __nv_bfloat16 *tail = p.tail + (size_t)p.slots[f.x] * 4 * p.ch + c;
-    float w[8][4], bias[8];
+    auto at = [&](int t) -> uint2 {
+        if (t >= f.w) return make_uint2(0u, 0u);
+        if (t >= 0) return *reinterpret_cast<const uint2 *>(raw + (size_t)t * p.ch);
+        return resume ? *reinterpret_cast<const uint2 *>(tail + (size_t)(4 + t) * p.ch) : make_uint2(0u, 0u);
+    };
+    uint2 rows[11];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int i = 0; i < 11; ++i) rows[i] = at(t0 - 3 + i);
+    float w[4][4], bias[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
         const float4 t = *reinterpret_cast<const float4 *>(p.conv_w + (size_t)(c + q) * 4);
         w[q][0] = t.x; w[q][1] = t.y; w[q][2] = t.z; w[q][3] = t.w;
         bias[q] = p.conv_b ? p.conv_b[c + q] : 0.0f;
     }
-    __nv_bfloat16 *out = p.act + ((size_t)me * kQ + sub * 16) * kAct;
-    auto at = [&](int t) -> uint4 {
-        if (t >= f.w) return make_uint4(0u, 0u, 0u, 0u);
-        if (t >= 0) return *reinterpret_cast<const uint4 *>(raw + (size_t)t * p.ch);
-        return resume ? *reinterpret_cast<const uint4 *>(tail + (size_t)(4 + t) * p.ch) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    uint4 rows[11];
+    __nv_bfloat16 *out = p.act + ((size_t)me * kQ + i0) * kAct;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) rows[i] = at(t0 - 3 + i);
-    for (int half = 0; half < 2; ++half) {
+    for (int i = 0; i < 8; ++i) {
+        float o[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rows[3 + i] = at(t0 + 8 * half + i);
+        for (int q = 0; q < 4; ++q) o[q] = bias[q];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = t0 + 8 * half + i;
-            float o[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = bias[q];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&rows[i + j]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 v = __bfloat1622float2(h[q]);
-                    o[2 * q] = fmaf(w[2 * q][j], v.x, o[2 * q]);
-                    o[2 * q + 1] = fmaf(w[2 * q + 1][j], v.y, o[2 * q + 1]);
-                }
-            }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 v = silu2(make_float2(o[2 * q], o[2 * q + 1]));
-                split2(t < f.w ? v : make_float2(0.0f, 0.0f), hi[q], lo[q]);
-            }
-            __nv_bfloat16 *row = out + (size_t)(8 * half + i) * kAct;
-            if (n0 < kN) {
-                *reinterpret_cast<uint4 *>(row + n0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(row + kN + n0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
-                *reinterpret_cast<uint4 *>(row + kN + n0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const float2 v0 = unpack2(rows[i + j].x), v1 = unpack2(rows[i + j].y);
+            o[0] = fmaf(w[0][j], v0.x, o[0]);
+            o[1] = fmaf(w[1][j], v0.y, o[1]);
+            o[2] = fmaf(w[2][j], v1.x, o[2]);
+            o[3] = fmaf(w[3][j], v1.y, o[3]);
         }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) rows[i] = rows[8 + i];
+        uint2 hi, lo;
+        const bool in = t0 + i < f.w;
+        const float2 zero = make_float2(0.0f, 0.0f);
+        split2(in ? silu2(make_float2(o[0], o[1])) : zero, hi.x, lo.x);
+        split2(in ? silu2(make_float2(o[2], o[3])) : zero, hi.y, lo.y);
+        __nv_bfloat16 *row = out + (size_t)i * kAct;
+        if (n0 < kN) {
+            *reinterpret_cast<uint2 *>(row + n0) = hi;
+            *reinterpret_cast<uint2 *>(row + kN + n0) = lo;
+        } else {
+            *reinterpret_cast<uint2 *>(row + kN + n0) = hi;
+        }
     }
 }
 
@@ -363,9 +357,9 @@ __global__ void __launch_bounds__(256)
 prompt_chain_kernel(const PromptParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int s = blockIdx.y;
-    const int2 seg = p.segs[s];
-    if (seg.y <= 1) return;
+    if (blockIdx.y >= p.head->cuts) return;
+    const int4 cut = p.cuts[blockIdx.y];
+    const int s = cut.x;
     const int e = blockIdx.x * 256 + threadIdx.x;   // float4 of the state
     const int per = p.H * kP * kN / 4;
     if (e >= per) return;
@@ -373,11 +367,11 @@ prompt_chain_kernel(const PromptParams p)
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (p.resume && p.resume[s] != 0)
         v = reinterpret_cast<const float4 *>(p.state)[(size_t)p.slots[s] * per + e];
-    float4 *st = reinterpret_cast<float4 *>(p.seg_state) + (size_t)seg.x * per + e;
+    float4 *st = reinterpret_cast<float4 *>(p.seg_state) + (size_t)cut.y * per + e;
     *st = v;
-    for (int i = 1; i < seg.y; ++i) {
+    for (int i = 1; i < cut.z; ++i) {
         st += per;
-        const float a = exp2f(p.seg_dec[(size_t)(seg.x + i) * p.H + h]);
+        const float a = exp2f(p.seg_dec[(size_t)(cut.y + i) * p.H + h]);
         const float4 q = *st;
         v.x = fmaf(a, v.x, q.x);
         v.y = fmaf(a, v.y, q.y);
@@ -1394,8 +1388,8 @@ namespace {
 constexpr int kSMs = 148;
 
 struct Layout {
-    int max_chunks, cut_over, seg_chunks, max_inner, max_walks, max_slots;
-    size_t head, walks, segs, act, dec, state, bytes;
+    int max_chunks, cut_over, seg_chunks, max_inner, max_walks, max_slots, max_cuts;
+    size_t head, walks, cuts, act, dec, state, bytes;
 };
 
 // How prompts are cut.  The pieces are as long as is best for one prompt of
@@ -1405,7 +1399,8 @@ struct Layout {
 // longer than these do: a piece's state-only walk, three chunks' time for two
 // more launches, and the GPU's share of the call (a fifth added: walks do not
 // fill it evenly).  1311, 1, 640, 129, 0, 2777, 63, 1024, 517, 1536 and 128
-// tokens in 64 heads: 150 us; with the 2777 in two pieces, 178.
+// tokens in 64 heads: 150 us, with the 2777 in two pieces 178 (both faster
+// since).
 void cut_of(long long chunks, int pairs, int &cut_over, int &seg_chunks)
 {
     const long long share = (chunks * pairs + kSMs - 1) / kSMs;
@@ -1435,6 +1430,7 @@ Layout layout_of(const bimamba_dims &d)
     l.max_inner = cut ? (int)(chunks / l.seg_chunks) : 0;
     l.max_walks = l.max_inner + d.batch;
     l.max_slots = 2 * l.max_inner;
+    l.max_cuts = l.max_chunks / (l.cut_over + 1);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -1443,7 +1439,7 @@ Layout layout_of(const bimamba_dims &d)
     };
     l.head = take(sizeof(PlanHeader));
     l.walks = take(sizeof(Walk) * (size_t)l.max_walks);
-    l.segs = take(sizeof(int2) * (size_t)d.batch);
+    l.cuts = take(sizeof(int4) * (size_t)l.max_cuts);
     l.act = take((size_t)l.max_chunks * kQ * kAct * 2);
     l.dec = take((size_t)l.max_slots * d.heads * 4);
     l.state = take((size_t)l.max_slots * d.heads * kP * kN * 4);
@@ -1492,7 +1488,7 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
     p.y = static_cast<__nv_bfloat16 *>(q.y);
     p.head = reinterpret_cast<PlanHeader *>(ws + l.head);
     p.walks = reinterpret_cast<Walk *>(ws + l.walks);
-    p.segs = reinterpret_cast<int2 *>(ws + l.segs);
+    p.cuts = reinterpret_cast<int4 *>(ws + l.cuts);
     p.act = reinterpret_cast<__nv_bfloat16 *>(ws + l.act);
     p.seg_dec = reinterpret_cast<float *>(ws + l.dec);
     p.seg_state = reinterpret_cast<float *>(ws + l.state);
@@ -1517,18 +1513,12 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
                                  (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     const int pairs = d.heads / 2;
-    prompt_prep_kernel<<<l.max_chunks + 1, kPrepThreads, 0, stream>>>(p);
+    prompt_prep_kernel<<<l.max_chunks * kPrepCtas + 1, kPrepThreads, 0, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launch();
-    if (l.max_inner > 0) {
-        prompt_walk_kernel<true><<<(unsigned)pairs * l.max_inner, kThreads, kSmemBytes, stream>>>(tm_x, tm_bc, tm_y, p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        prompt_chain_kernel<<<dim3(d.heads * kP * kN / 4 / 256, d.batch), 256, 0, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        count_launch(2);
-    }
+    // both walks as programmatic launches: their set-up runs beside the end of
+    // the kernel before
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pairs * l.max_walks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
@@ -1537,6 +1527,14 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (l.max_inner > 0) {
+        cfg.gridDim = dim3((unsigned)pairs * l.max_inner);
+        if ((e = cudaLaunchKernelEx(&cfg, prompt_walk_kernel<true>, tm_x, tm_bc, tm_y, p)) != cudaSuccess) return e;
+        prompt_chain_kernel<<<dim3(d.heads * kP * kN / 4 / 256, l.max_cuts), 256, 0, stream>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        count_launch(2);
+    }
+    cfg.gridDim = dim3((unsigned)pairs * l.max_walks);
     if ((e = cudaLaunchKernelEx(&cfg, prompt_walk_kernel<false>, tm_x, tm_bc, tm_y, p)) != cudaSuccess) return e;
     count_launch();
     return cudaSuccess;
