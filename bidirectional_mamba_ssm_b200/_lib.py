@@ -396,9 +396,10 @@ def _call(where, fn, stream, before, specs, args, after):
     CUDA device (or None itself); where the spec is None the argument stands
     for itself.  That device is made current for the call: the kernels launch
     there, on its current stream unless one is given."""
-    index = args[0].get_device()
+    lead = args[0] if args[0] is not None else args[1]   # (a missing one is the library's to refuse)
+    index = lead.get_device()
     if index < 0:
-        raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: a CUDA tensor is wanted, got one on {args[0].device}")
+        raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: a CUDA tensor is wanted, got one on {lead.device}")
     out = []
     for spec, t in zip(specs, args):
         if t is None or spec is None:
@@ -407,7 +408,7 @@ def _call(where, fn, stream, before, specs, args, after):
         if t.dtype is not spec[1] or t.shape != spec[2] or t.get_device() != index or not t.is_contiguous():
             name, dtype, shape = spec
             raise BimambaError(BIMAMBA_ERR_INVALID, f"{where}: {name}: a dense {dtype} tensor of shape {tuple(shape)} "
-                               f"on {args[0].device} is wanted, got {t.dtype} {tuple(t.shape)} with strides "
+                               f"on {lead.device} is wanted, got {t.dtype} {tuple(t.shape)} with strides "
                                f"{t.stride()} on {t.device}")
         out.append(t.data_ptr())
     # (the raw handle: a Stream object takes 3 us to make, a fifth of a call)

@@ -403,9 +403,9 @@ layer_norm_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ h, const f
     }
 }
 
-// dg / db = sum over the partial rows.  A CTA owns 32 columns; its 16 warps
-// take every 16th partial row, then join in order.
-constexpr int kJoinWarps = 16;
+// dg / db = sum over the partial rows.  A CTA owns 32 columns; its 32 warps
+// take every 32nd partial row, then join in order.
+constexpr int kJoinWarps = 32;
 
 __global__ void __launch_bounds__(32 * kJoinWarps)
 layer_norm_join_kernel(const float *__restrict__ part, float *__restrict__ dgamma, float *__restrict__ dbeta,

@@ -108,7 +108,7 @@ template <typename T>
 __global__ void __launch_bounds__(kActThreads)
 prompt_act_kernel(const PromptProblem q, float *__restrict__ act, float4 *__restrict__ dec)
 {
-    __shared__ int owner[kActRows];   // each row's prompt, or -1
+    __shared__ int owner[kActRows], token[kActRows];   // each row's prompt, or -1, and its token there
     const int tid = threadIdx.x;
     const int r0 = blockIdx.x * kActRows;
     const int H = q.dims.heads, ch = H * q.dims.headdim + 2 * q.dims.d_state;
@@ -117,25 +117,30 @@ prompt_act_kernel(const PromptProblem q, float *__restrict__ act, float4 *__rest
     for (int s = tid; s < q.dims.batch; s += kActThreads) {
         const Range r = read_range(q, s);
         if (!r.ok) continue;
-        for (int i = max(r.begin - r0, 0); i < min(r.begin + r.len - r0, kActRows); ++i) owner[i] = s;
+        for (int i = max(r.begin - r0, 0); i < min(r.begin + r.len - r0, kActRows); ++i) {
+            owner[i] = s;
+            token[i] = r0 + i - r.begin;
+        }
     }
     __syncthreads();
     const int c = blockIdx.y * kActThreads + tid;
     if (c < ch) {
         const float4 w = *reinterpret_cast<const float4 *>(q.conv_w + (size_t)c * 4);
         const float bias = q.conv_b ? q.conv_b[c] : 0.0f;
-        for (int i0 = 0; i0 < kActRows; i0 += 8) {
+        const T *src = static_cast<const T *>(q.xbc) + ((size_t)r0 * ch + c);
+        float *dst = act + ((size_t)r0 * ch + c);
+        for (int i0 = 0; i0 < kActRows; i0 += 8, src += (size_t)8 * ch, dst += (size_t)8 * ch) {
             float raw[11];   // requested together
 #pragma unroll
             for (int i = 0; i < 11; ++i) {
                 const int row = r0 + i0 + i - 3;
-                raw[i] = row >= 0 && row < q.dims.len ? Elem<T>::load(static_cast<const T *>(q.xbc) + (size_t)row * ch + c) : 0.0f;
+                raw[i] = row >= 0 && row < q.dims.len ? Elem<T>::load(src + (long long)(i - 3) * ch) : 0.0f;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int s = owner[i0 + i];
                 if (s < 0) continue;
-                const int t = r0 + i0 + i - q.cu_seqlens[s];
+                const int t = token[i0 + i];
                 float v[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
                 if (t < 3) {   // tokens before the prompt: its entry's tail, or zeros
                     const bool resume = q.resume && q.resume[s] != 0;
@@ -149,7 +154,7 @@ prompt_act_kernel(const PromptProblem q, float *__restrict__ act, float4 *__rest
                 a = fmaf(w.y, v[1], a);
                 a = fmaf(w.z, v[2], a);
                 a = fmaf(w.w, v[3], a);
-                act[(size_t)(r0 + i0 + i) * ch + c] = silu_f(a);
+                dst[(size_t)i * ch] = silu_f(a);
             }
         }
     }

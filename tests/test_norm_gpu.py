@@ -224,3 +224,15 @@ def test_captured_and_on_another_stream(lib):
         assert torch.equal(p, q)
     h, m, r, want = _forward(new, True, True)
     _close(got[0], want, torch.bfloat16, 8.0, "y")
+
+
+def test_the_binding_refuses_missing_and_other_tensors(lib):
+    x = torch.zeros((2, 8), device="cuda")
+    v, r = torch.zeros(8, device="cuda"), torch.zeros(2, device="cuda")
+    ws = lib.new_layer_norm_workspace(x)
+    call = lambda dy, h=x: lib.bimamba_layer_norm_backward(dy, h, v, r, r, x.clone(), v.clone(), None, ws)  # noqa: E731
+    for dy in (None, x[:, ::2], x.double(), x[:1], x.cpu()):
+        with pytest.raises(lib.BimambaError):
+            call(dy)
+    with pytest.raises(lib.BimambaError):
+        call(torch.zeros((), device="cuda"), torch.zeros((), device="cuda"))
