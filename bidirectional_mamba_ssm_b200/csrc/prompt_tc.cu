@@ -52,8 +52,8 @@
 // of G or M X, or freeing (w o X)^T a quarter at a time, gains nothing: the
 // conv, M and the row work then wait for the same issue slots.  A walk's
 // beginning and end take about 13 us besides.
-// Measured, 64 heads: 8 prompts of 4096 tokens 350 us, one of 32768 505, 11
-// ragged ones of 8126 in all 133, 37 tokens 25 (18 of them the host's call).
+// Measured, 64 heads: 8 prompts of 4096 tokens 345 us, one of 32768 500, 11
+// ragged ones of 8126 in all 131, 37 tokens 25 (18 of them the host's call).
 #include "common.cuh"
 #include "dispatch.h"
 #include "tc_ptx.cuh"
@@ -356,6 +356,9 @@ prompt_prep_kernel(const PromptParams p)
 __global__ void __launch_bounds__(256)
 prompt_chain_kernel(const PromptParams p)
 {
+    // (a programmatic launch; the walks behind it may start once the state-only
+    // ones are done: before that they would take their places)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.y >= p.head->cuts) return;
     const int4 cut = p.cuts[blockIdx.y];
@@ -596,6 +599,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         tc::mbar_init(mb_free0 + 8, 3);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (kStateOnly) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Walk wk = p.walks[wi];   // (requested beside the table's length: the table has an entry for every CTA)
     if (wi >= (kStateOnly ? p.head->inner : p.head->total)) return;
     const int slot = wk.entry, begin = wk.begin, len = wk.len;
@@ -1516,8 +1520,7 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
     prompt_prep_kernel<<<l.max_chunks * kPrepCtas + 1, kPrepThreads, 0, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launch();
-    // both walks as programmatic launches: their set-up runs beside the end of
-    // the kernel before
+    // programmatic launches: set-up and launch beside the end of the kernel before
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
@@ -1530,8 +1533,13 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
     if (l.max_inner > 0) {
         cfg.gridDim = dim3((unsigned)pairs * l.max_inner);
         if ((e = cudaLaunchKernelEx(&cfg, prompt_walk_kernel<true>, tm_x, tm_bc, tm_y, p)) != cudaSuccess) return e;
-        prompt_chain_kernel<<<dim3(d.heads * kP * kN / 4 / 256, l.max_cuts), 256, 0, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        cudaLaunchConfig_t chain = {};
+        chain.gridDim = dim3(d.heads * kP * kN / 4 / 256, l.max_cuts);
+        chain.blockDim = dim3(256);
+        chain.stream = stream;
+        chain.attrs = attr;
+        chain.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&chain, prompt_chain_kernel, p)) != cudaSuccess) return e;
         count_launch(2);
     }
     cfg.gridDim = dim3((unsigned)pairs * l.max_walks);
