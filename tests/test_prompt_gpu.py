@@ -363,3 +363,22 @@ def test_ranges_of_the_same_rows(lib, dtype):
     assert torch.isfinite(s).all() and torch.isfinite(t).all()
     d = ref.draw(100, 1, *shape, dtype, seed=9, pool=2)
     _check(lib, d, [100], [1], shape)
+
+
+def test_several_long_prompts(lib):
+    """Prompts cut into segments of many chunks beside short and empty ones;
+    then two of them naming one entry, which are skipped and reported."""
+    shape, lens, resume = (2, 64, 128), [2600, 5, 9000, 0, 3000], [1, 0, 1, 1, 0]
+    d = ref.draw(sum(lens), 5, *shape, torch.bfloat16, seed=21, pool=6, a_range=(1e-3, 1e-2))
+    y, s, t = _check(lib, d, lens, resume, shape)
+    slots = d["slots"].tolist()
+    y2, s2, t2 = ref.run(lib, dict(d, slots=torch.tensor(slots[:4] + slots[:1], dtype=torch.int32)), lens, resume,
+                         *shape)
+    assert lib.bimamba_get_error() == lib.BIMAMBA_ERR_INVALID
+    assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+    assert torch.isnan(y2[:2600]).all() and torch.isnan(y2[-3000:]).all()
+    assert torch.equal(y2[2600:-3000], y[2600:-3000])
+    for k in (slots[0], slots[4]):
+        assert torch.equal(s2[k].cpu(), d["state"][k]) and torch.equal(t2[k].cpu(), d["tail"][k])
+    for k in slots[1:4]:
+        assert torch.equal(s2[k], s[k]) and torch.equal(t2[k], t[k])
