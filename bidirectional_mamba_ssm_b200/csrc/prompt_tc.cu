@@ -14,9 +14,17 @@
 //     Y       = exp(c_t) (C S^T) + M X
 //     S      <- exp(c_last) S + (w o X)^T B,    w_s = exp(c_last - c_s) dt_s
 //
-// Precision.  y is stored in bf16, so its operands (C, B, X, M, a copy of S)
-// are bf16.  The state is kept and handed on in fp32 over any number of
-// tokens, so its update is not: w o X and B enter as two bf16 halves each
+// Precision.  y is to be as exact as fp32 sums rounded once to bf16: 1.7e-3
+// from 64 bits in the 2-norm (2.9e-3, and 3.4e-3 on long prompts, when M, X,
+// C and the state entered as bf16).  So X, M (with D on its diagonal), C and
+// the copy of S in C S^T are fp16 operands, 2^-12 each, times powers of two that
+// keep them inside fp16's range: X kXUnit (a channel whose values do not fit
+// that in a chunk one of its own, see repair), M one a row from bounds of its
+// factors, C one a token, S one a head from a bound that is carried along (a row
+// far from the others its own).  B and C in G are bf16: they touch only the part
+// of y that stays within the chunk.  The state is kept and handed on in fp32
+// over any number of tokens, so its update is not rounded to 16 bits: w o X and
+// B enter as two bf16 halves each
 // (value = hi + lo to 2^-17) and three products, hi hi + lo hi + hi lo; the
 // conv, SiLU and decays before them are fp32, exp(c_last - c_s) comes from
 // suffix sums (no cancellation where it matters), a slow decay is applied as
@@ -24,42 +32,48 @@
 // added once, rounding to nearest (the tensor core's sums drop what falls
 // below the accumulator's last bit: onto the state itself, thousands of such
 // steps were off by 2e-5 after 32768 tokens).  So no error adds up with the
-// number of chunks.
+// number of chunks.  A value below 2^-29 of its scale keeps fewer than 11 bits:
+// an activation below 2^-24 in a chunk of larger ones, or far below its
+// channel's largest where that is past 2^8.
 //
 // A token's infinity or NaN must not reach the rows before it, but in M X it
 // meets their zeros (0 inf = NaN): such values enter X as zeros, and the rows
-// from their token on are set to NaN when they are stored.
+// from their token on are set to NaN when they are stored (repair, stage_rows).
 //
 // Kernels of one call:
 //   1. plan + conv of B and C: per 128-token chunk the operand rows
-//      [B hi | B lo | C] (zeros behind the prompt's end, so that a neighbour
-//      never enters a product), and, by one CTA, the table of walks.  All of
+//      [B hi | B lo | C | C in fp16] and their exponents (zeros behind the
+//      prompt's end, so that a neighbour never enters a product), and, by one
+//      CTA, the table of walks.  All of
 //      it latency (7 us for 68 chunks of 11 prompts): short loops, few scans.
 //   2. only where a prompt may be long against the GPU's share of the work
 //      (segment_chunks): prompts above that are cut into equal segments; a
 //      state-only walk of each segment but the last, then
 //   3. the states that enter the segments, chained over them.
-//   4. one walk per (segment, head pair): all products on tcgen05, the state
-//      in tensor memory.
+//   4. one walk per (segment, head pair): all products on tcgen05, their sums
+//      in tensor memory, the state in registers.
 //
 // Bounds of the walk, per chunk and head pair: 56 MMAs of 65 cycles (8 G, 8
-// C S^T, 16 M X, 24 state) = 3.6K cycles, about 18K warp instructions (conv
-// and SiLU, operand splitting, M, state and output scaling) = 4.5K cycles of
+// C S^T, 16 M X, 24 state) = 3.6K cycles, about 20K warp instructions (conv
+// and SiLU, operand splitting, M, state and output scaling) = 5K cycles of
 // the four schedulers, and HBM 66 KB = 1.5K cycles at the SM's share.  It
-// takes 8.4K: the chain from one chunk's state product to the next's (copy of
+// takes 8.9K: the chain from one chunk's state product to the next's (copy of
 // the state, C S^T, scaled rows, M X, G), of which the latencies of the
 // products and the hand-offs are half.  Issuing the next state product ahead
 // of G or M X, or freeing (w o X)^T a quarter at a time, gains nothing: the
 // conv, M and the row work then wait for the same issue slots.  A walk's
 // beginning and end take about 13 us besides.
-// Measured, 64 heads: 8 prompts of 4096 tokens 345 us, one of 32768 500, 11
-// ragged ones of 8126 in all 131, 37 tokens 25 (18 of them the host's call).
+// Measured, 64 heads, calls one after another on the same buffers: 8 prompts of
+// 4096 tokens 374 us, one of 32768 534, 11 ragged ones of 8126 in all 136, 37
+// tokens 22.5 (18 of them the host's call).  (With bf16 operands throughout 361,
+// 540, 127 and 21.)
 #include "common.cuh"
 #include "dispatch.h"
 #include "tc_ptx.cuh"
 
 #include <algorithm>
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 namespace bimamba {
@@ -69,7 +83,9 @@ namespace {
 constexpr int kQ = 128;            // tokens per chunk
 constexpr int kP = 64, kN = 128;   // headdim and d_state of this path
 constexpr int kPP = 2 * kP;        // x channels of a head pair
-constexpr int kAct = 3 * kN;       // operand row: B hi | B lo | C
+constexpr int kAct = 4 * kN;       // operand row: B hi | B lo | C | C in fp16, scaled
+constexpr int kXUnit = 256;        // what X^T is multiplied by, see the top
+constexpr float kFltMax = 3.402823466e38f;
 constexpr int kRawRows = kQ + 3;   // raw x rows of a chunk with the conv halo
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -98,6 +114,7 @@ struct PromptParams {
     float *state;            // pool
     __nv_bfloat16 *tail;     // pool
     __nv_bfloat16 *y, *act;
+    uint8_t *b_exp, *c_exp;  // per operand row: biased exponent of the largest of its B; of what its fp16 C is to be multiplied by
     PlanHeader *head;
     Walk *walks;
     int4 *cuts;              // per prompt in segments: prompt, first slot, segments
@@ -167,9 +184,10 @@ __device__ __forceinline__ float rcp_approx(float v)
 
 // a sigmoid(a) of two values, off by a few 2^-23 (the hardware tanh's 2^-11
 // would do for y but not for the state).
-__device__ __forceinline__ float2 silu2(float2 a)
+// kUnit: a and the result are kUnit times what they stand for.
+template <int kUnit = 1> __device__ __forceinline__ float2 silu2(float2 a)
 {
-    const float2 t = tc::mul2(a, make_float2(-kLog2e, -kLog2e));
+    const float2 t = tc::mul2(a, make_float2(-kLog2e / kUnit, -kLog2e / kUnit));
     const float2 d = tc::fma2(make_float2(tc::exp2_approx(t.x), tc::exp2_approx(t.y)), make_float2(1.0f, 1.0f),
                               make_float2(1.0f, 1.0f));
     return tc::mul2(a, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
@@ -186,6 +204,43 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo)
     hi = tc::pack_bf16x2(v.x, v.y);
     const float2 rest = tc::fma2(unpack2(hi), make_float2(-1.0f, -1.0f), v);
     lo = tc::pack_bf16x2(rest.x, rest.y);
+}
+
+// What brings values of at most 2^128 below 2^15, as fp16 operands (11 bits,
+// and below 2^-29 of the largest one a fixed grain): the power of two for
+// values whose largest has biased exponent `e` (kLeastExp at least, so that
+// both factors are normal numbers), and the biased exponent of its inverse.
+constexpr uint32_t kLeastExp = 15, kMostExp = 187;
+__device__ __forceinline__ float fp16_scale(uint32_t e) { return __uint_as_float((268u - e) << 23); }
+__device__ __forceinline__ uint32_t fp16_unscale_exp(uint32_t e) { return e - 14u; }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float log2_approx(float v)
+{
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The largest of three magnitudes (a NaN does not count).
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 4 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
 }
 
 // Store 4 consecutive 32-bit columns of this thread's TMEM lane (no wait).
@@ -338,14 +393,23 @@ prompt_prep_kernel(const PromptParams p)
         uint2 hi, lo;
         const bool in = t0 + i < f.w;
         const float2 zero = make_float2(0.0f, 0.0f);
-        split2(in ? silu2(make_float2(o[0], o[1])) : zero, hi.x, lo.x);
-        split2(in ? silu2(make_float2(o[2], o[3])) : zero, hi.y, lo.y);
+        const float2 a0 = in ? silu2(make_float2(o[0], o[1])) : zero, a1 = in ? silu2(make_float2(o[2], o[3])) : zero;
+        split2(a0, hi.x, lo.x);
+        split2(a1, hi.y, lo.y);
         __nv_bfloat16 *row = out + (size_t)i * kAct;
+        // (a token's B, and its C, is a warp's)
+        const uint32_t big = __float_as_uint(fmaxf(fmaxf(fabsf(a0.x), fabsf(a0.y)), fmaxf(fabsf(a1.x), fabsf(a1.y))));
+        const uint32_t e = max(__reduce_max_sync(0xffffffffu, big) >> 23, kLeastExp);
         if (n0 < kN) {
             *reinterpret_cast<uint2 *>(row + n0) = hi;
             *reinterpret_cast<uint2 *>(row + kN + n0) = lo;
+            if (n0 == 0) p.b_exp[(size_t)me * kQ + i0 + i] = (uint8_t)e;
         } else {
             *reinterpret_cast<uint2 *>(row + kN + n0) = hi;
+            const float2 s2 = make_float2(fp16_scale(e), fp16_scale(e));
+            const float2 c0 = tc::mul2(a0, s2), c1 = tc::mul2(a1, s2);
+            *reinterpret_cast<uint2 *>(row + 2 * kN + n0) = make_uint2(pack_f16x2(c0.x, c0.y), pack_f16x2(c1.x, c1.y));
+            if (n0 == kN) p.c_exp[(size_t)me * kQ + i0 + i] = (uint8_t)fp16_unscale_exp(e);
         }
     }
 }
@@ -388,9 +452,9 @@ namespace {
 
 // ---- the walk kernel's shared memory (bytes from a 1024-aligned base)
 constexpr uint32_t kTile = 32768;                   // 128 x 128 bf16: two 64-wide swizzled blocks
-constexpr uint32_t kOffC = 0;                       // C  [t][n]
+constexpr uint32_t kOffC = 0;                       // C  [t][n]: bf16 for G, then fp16 for C S^T
 constexpr uint32_t kOffBh = kOffC + kTile;          // B hi [s][n]
-constexpr uint32_t kOffBl = kOffBh + kTile;         // B lo [s][n], then the bf16 copy of the state [p'][n]
+constexpr uint32_t kOffBl = kOffBh + kTile;         // B lo [s][n], then the fp16 copy of the state [p'][n]
 constexpr uint32_t kOffX0 = kOffBl + kTile;         // X^T [p'][s], then the finished rows: even chunks
 constexpr uint32_t kOffX1 = kOffX0 + kTile;         // odd chunks
 constexpr uint32_t kOffRaw1 = kOffX1;               // raw x [131][128] of odd chunks (state-only walk: no X^T)
@@ -399,24 +463,39 @@ constexpr uint32_t kRawBytes = kRawRows * kPP * 2;
 static_assert(kOffRaw1 + kRawBytes <= kOffRaw, "raw buffers");
 constexpr uint32_t kOffFac = kOffRaw + kRawBytes;   // per-slot factors, f32 [2 parity][2 head][128] each:
 constexpr uint32_t kFac = 2 * 2 * kQ * 4;
-constexpr int kParts = 5;                           // of a chunk's units: 3 x 4 (X group), 2 x 2 (M group)
 constexpr uint32_t kOffCum = kOffFac;               //   prefix sums of dt A, log2 units
 constexpr uint32_t kOffDt = kOffCum + kFac;         //   dt
 constexpr uint32_t kOffFB = kOffDt + kFac;          //   exp(c_R - c_s) dt_s, R = end of s's 32-slot block
 constexpr uint32_t kOffF4 = kOffFB + kFac;          //   exp(c_R4 - c_s) dt_s, R4 = s | 3
-constexpr uint32_t kOffWgt = kOffF4 + kFac;         //   w_s
-constexpr uint32_t kOffScale = kOffWgt + kFac;      // float2 [2 parity][2 head]: see next_state
-constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][part][128]: first token of X not finite (128: none)
-constexpr uint32_t kOffAnyBad = kOffBad + 2 * kParts * kPP;   // int [2 parity][X, M group]
+constexpr uint32_t kOffWgt = kOffF4 + kFac;         //   w_s / kXUnit
+constexpr uint32_t kOffColF = kOffWgt + kFac;       // float [128]: what takes a state row's own scale from a column of C S^T
+constexpr uint32_t kOffSMax = kOffColF + kPP * 4;   // float [2][128]: largest of a state row's halves
+constexpr uint32_t kOffCExp = kOffSMax + 8 * kPP;   // u8 [2 parity][128]: c_exp
+constexpr uint32_t kOffMUnit = kOffCExp + 2 * kQ;   // float [2 parity][2 head][128]: what M's rows are multiplied by
+constexpr uint32_t kOffXFac = kOffMUnit + kFac;     // float [2 parity][128]: what channels of X^T are multiplied by besides, see repair
+constexpr uint32_t kOffGrow = kOffXFac + 2 * kPP * 4;   // float [2 parity][2 head]: what the chunk adds to the state for |x| = 1 at most
+constexpr uint32_t kOffXMost = kOffGrow + 16;       // float [2 parity]: bound of the finite |x|
+constexpr uint32_t kOffSeen = kOffXMost + 8;        // int: last chunk + 1 with a value from 2^-12 on in X^T
+constexpr uint32_t kOffMOff = kOffSeen + 4;         // int: the M group's share of X^T is not as it should be
+constexpr uint32_t kOffAgain = kOffMOff + 4;        // int: X^T has to be made again
+constexpr uint32_t kOffWMax = kOffAgain + 16;       // float [2 head][4]: largest of a Y warp's state values
+constexpr uint32_t kOffHeadF = kOffWMax + 32;       // float [2 head]: what takes the state copy's scale from C S^T
+constexpr uint32_t kOffRowwise = kOffHeadF + 8;     // int [2 head], see choose_scale
+constexpr uint32_t kOffScale = kOffRowwise + 8;     // float2 [2 parity][2 head]: see next_state
+constexpr uint32_t kOffBad = kOffScale + 32;        // u8 [2 parity][3][128]: first token of X not finite (128: none), see repair
+constexpr uint32_t kOffAnyBad = kOffBad + 6 * kPP;  // int [2 parity]: there is one; int [2 parity]: kOffXFac is not all 1
 constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
 constexpr uint32_t kOffTaps = kOffDtBuf + 2 * kQ * 4;   // float4 [128] conv taps, float [128] biases, float [2] D, float [3][128] halo
 constexpr uint32_t kOffMbar = kOffTaps + kPP * 20 + 8 + 3 * kPP * 4;
-constexpr uint32_t kOffTmem = kOffMbar + 160;
+constexpr uint32_t kOffTmem = kOffMbar + 176;
 constexpr uint32_t kStateRow = kN * 4 + 16;         // a row of the last state on its way out: 16-byte stores of
 static_assert(kPP * kStateRow <= 3 * kTile, "state rows");   // 8 threads' rows meet no bank twice
 
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
-static_assert(kOffRaw % 1024 == 0 && kOffFac % 16 == 0 && kOffMbar % 8 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kOffRaw % 1024 == 0 && kOffFac % 16 == 0 && kOffColF % 16 == 0 && kOffCExp % 4 == 0 && kOffMUnit % 16 == 0 &&
+                  kOffXFac % 4 == 0 && kOffWMax % 16 == 0 &&
+                  kOffScale % 8 == 0 && kOffAnyBad % 4 == 0 && kOffDtBuf % 16 == 0 && kOffTaps % 16 == 0 && kOffMbar % 8 == 0 &&
+                  kOffTmem % 4 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 
 // ---- tensor memory columns
 constexpr uint32_t kColG = 0;      // G, then in place [M_0 | M_1] per 16 tokens (8 + 8 columns of bf16 pairs)
@@ -564,6 +643,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const uint32_t mb_dt0 = mb + 112;     // factors ready
     const uint32_t mb_free0 = mb + 128;   // their buffer free
     const uint32_t mb_xf0 = mb + 144;     // X^T's buffer free (the rows over it stored)
+    const uint32_t mb_c16 = mb + 160;     // [k] fp16 C landed
+    const uint32_t mb_mc = mb + 168;      // [k] the M group's share of X^T ready
     auto of = [](uint32_t pair, int k) { return pair + 8 * (k & 1); };
     auto phase = [](int k) -> uint32_t { return (k >> 1) & 1; };   // of a pair's barrier
     auto xbuf = [](int k) { return (k & 1) ? kOffX1 : kOffX0; };
@@ -591,6 +672,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (b != mb_g && b != mb_w0 && b != mb_w0 + 8) tc::mbar_init(b, 1);
         tc::mbar_init(mb_w0, 2);       // the X and the M group
         tc::mbar_init(mb_w0 + 8, 2);
+        tc::mbar_init(mb_c16, 1);
+        tc::mbar_init(mb_mc, 1);
         tc::mbar_init(mb_xf0, 1);
         tc::mbar_init(mb_xf0 + 8, 1);
         tc::mbar_init(mb_dt0, 32);
@@ -633,6 +716,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     auto issue_bh = [&](int k) { issue_tile(k, bh_off(k), 0, b_bar(k)); };
     auto issue_bl = [&](int k) { issue_tile(k, bl_off(k), kN, b_bar(k)); };
     auto issue_c = [&](int k) { issue_tile(k, kOffC, 2 * kN, mb_bc); };
+    auto issue_c16 = [&](int k) { issue_tile(k, kOffC, 3 * kN, mb_c16); };
 
     // helper warp: dt of both heads (adjacent: one 4-byte copy per token)
     auto load_dt_async = [&](int k) {
@@ -670,10 +754,12 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
     if (warp == 0) tc::tmem_alloc(sbase + kOffTmem, 512);
     if (tid < kPP) {
-        taps[tid] = my_taps;
-        biases[tid] = my_bias;
+        taps[tid] = make_float4(kXUnit * my_taps.x, kXUnit * my_taps.y, kXUnit * my_taps.z, kXUnit * my_taps.w);
+        biases[tid] = kXUnit * my_bias;
     }
     if (tid < 2) biases[kPP + tid] = p.D[2 * hp + tid];
+    if (tid == 0) *reinterpret_cast<int *>(sm + kOffSeen) = 0;
+    if (tid < 2) reinterpret_cast<int *>(sm + kOffRowwise)[tid] = 0;
     // the 3 tokens before the walk's first chunk where they are not in the raw
     // tile: the prompt's entry's tail, or zeros
     const bool starts = wk.chunk == 0;
@@ -703,10 +789,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // conv + SiLU of channel p' = pr, units ua .. ub - 1 (8 tokens each) of
     // chunk k: X^T to shared memory, both halves of (w o X)^T to tensor
     // memory (lane = channel, so that a thread's tokens are consecutive:
-    // 16-byte stores of X^T, and the A operand's layout).  Returns whether an
-    // activation was not finite (it enters X^T as zero; the first such token
-    // goes to bad_at).
-    auto conv_units = [&](int k, int pr, int ua, int ub, int part) -> bool {
+    // 16-byte stores of X^T, and the A operand's layout).  Returns whether a
+    // value is not finite, in X^T's fp16 with kXUnit at least.
+    auto conv_units = [&](int k, int pr, int ua, int ub) -> bool {
         const int par = k & 1;
         const float4 w4 = taps[pr];
         const float bias = biases[pr];
@@ -731,7 +816,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const float2 wa = make_float2(w4.x, w4.x), wc = make_float2(w4.z, w4.z), b2 = make_float2(bias, bias);
         // unit u's 16 bytes of X^T's row
         auto piece = [&](int u) { return (u >> 3) * (kTile / 2) + tc::sw128(pr, u & 7); };
-        __nv_bfloat162 check = __float2bfloat162_rn(0.0f);   // NaN once an activation is not finite
+        [[maybe_unused]] __half2 check = __float2half2_rn(0.0f);   // NaN once a value is not finite in fp16
+        [[maybe_unused]] uint32_t bits = 0u;                       // of all of them
 #pragma unroll 2
         for (int u = ua; u < ub; ++u) {
             float v[11];
@@ -748,7 +834,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             v0 = v[8]; v1 = v[9]; v2 = v[10];
             const float4 w01 = *reinterpret_cast<const float4 *>(ws + 8 * u);
             const float4 w23 = *reinterpret_cast<const float4 *>(ws + 8 * u + 4);
-            uint32_t hi[4], lo[4], xp[4];
+            uint32_t hi[4], lo[4];
+            [[maybe_unused]] uint32_t xp[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // tokens 2 j, 2 j + 1 of the unit: taps 0 and 2 as packed pairs
@@ -758,11 +845,11 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 a.y = fmaf(w4.y, v[2 * j + 2], a.y);
                 a.x = fmaf(w4.w, v[2 * j + 3], a.x);
                 a.y = fmaf(w4.w, v[2 * j + 4], a.y);
-                const float2 x = silu2(a);
+                const float2 x = silu2<kXUnit>(a);
                 if constexpr (!kStateOnly) {
-                    xp[j] = tc::pack_bf16x2(x.x, x.y);
-                    check = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&xp[j]), __float2bfloat162_rn(0.0f),
-                                    check);
+                    xp[j] = pack_f16x2(x.x, x.y);
+                    check = __hfma2(*reinterpret_cast<const __half2 *>(&xp[j]), __float2half2_rn(0.0f), check);
+                    bits |= xp[j];
                 }
                 const float2 w = j == 0 ? make_float2(w01.x, w01.y) : j == 1 ? make_float2(w01.z, w01.w)
                                : j == 2 ? make_float2(w23.x, w23.y) : make_float2(w23.z, w23.w);
@@ -773,25 +860,63 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             tmem_st4_nw(wcol + 4 * u, hi);
             tmem_st4_nw(wcol + 64 + 4 * u, lo);
         }
-        bool bad = false;
         if constexpr (!kStateOnly) {
-            bad = !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
-            int at = kQ;
-            if (bad) {
-                for (int i = 8 * ub - 1; i >= 8 * ua; --i) {
-                    uint16_t *v = reinterpret_cast<uint16_t *>(xt + piece(i >> 3)) + (i & 7);
-                    if ((*v & 0x7f80u) == 0x7f80u) {
-                        *v = 0;
-                        at = i;
-                    }
-                }
-            }
-            bad_at[(par * kParts + part) * kPP + pr] = (uint8_t)at;
+            const bool seen = ((bits | bits >> 16) & 0x7c00u) >= 0x0c00u;   // (2^-12)
+            if (__any_sync(0xffffffffu, seen) && lane == 0) *reinterpret_cast<volatile int *>(sm + kOffSeen) = k + 1;
         }
         tc::tmem_wait_st();
         if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
         tc::fence_before_sync();
-        return bad;
+        return !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
+    };
+    // X^T of chunk k once more (rare), by the X group, all 16 units of 8 tokens
+    // from the raw rows: values that are not finite as zeros, the first such
+    // token of a channel noted in bad_at; a channel whose largest value is past
+    // fp16's range or near its small end times a power of two of its own.
+    float *xfac = reinterpret_cast<float *>(sm + kOffXFac);
+    auto repair = [&](int k, int third, int pr) {
+        const int par = k & 1;
+        const float4 w4 = taps[pr];
+        const int rows = tokens(k) + 3;
+        const uint16_t *raw = reinterpret_cast<const uint16_t *>(sm + raw_off(k)) + pr;
+        auto row = [&](int t) -> float {   // as in conv_units
+            return t < 3 && k == 0 && starts ? halo[t * kPP + pr]
+                 : t < rows ? __uint_as_float(static_cast<uint32_t>(raw[t * kPP]) << 16) : 0.0f;
+        };
+        auto x = [&](int i) -> float {   // of token i, in the same steps as there
+            const float a = fmaf(w4.w, row(i + 3), fmaf(w4.y, row(i + 1), fmaf(w4.z, row(i + 2), fmaf(w4.x, row(i), biases[pr]))));
+            return silu2<kXUnit>(make_float2(a, a)).x;
+        };
+        uint32_t *most = reinterpret_cast<uint32_t *>(xfac + par * kPP + pr);   // (zeros until then)
+        float big = 0.0f;
+        int at = kQ;
+        if (third == 0) *most = 0u;
+        grp_sync<kXGroup>(3);
+#pragma unroll 1
+        for (int i = third; i < kQ; i += 3) {
+            const float v = fabsf(x(i));
+            if (v <= kFltMax) big = fmaxf(big, v);
+            else at = min(at, i);
+        }
+        bad_at[(par * 3 + third) * kPP + pr] = (uint8_t)at;
+        if (at < kQ) any_bad[par] = 1;
+        atomicMax(most, __float_as_uint(big));
+        atomicMax(reinterpret_cast<uint32_t *>(sm + kOffXMost) + par, __float_as_uint(big * (1.0f / kXUnit)));
+        grp_sync<kXGroup>(3);
+        big = __uint_as_float(*most);
+        const bool own = big >= 65504.0f || (big < 0x1p-12f && big != 0.0f);
+        const float f = own ? __uint_as_float(min(max(268u - (__float_as_uint(big) >> 23), 127u - 113u), 127u + 40u) << 23) : 1.0f;
+        if (own) any_bad[2 + par] = 1;
+        grp_sync<kXGroup>(3);
+        if (third == 0) xfac[par * kPP + pr] = f;
+        __half *xt = reinterpret_cast<__half *>(sm + xbuf(k));
+#pragma unroll 1
+        for (int i = third; i < kQ; i += 3) {
+            const float v = x(i);
+            xt[(i >> 6) * (kTile / 4) + tc::sw128(pr, i >> 3 & 7) / 2 + (i & 7)] = __float2half_rn(fabsf(v) <= kFltMax ? f * v : 0.0f);
+        }
+        tc::fence_proxy_async();
+        grp_sync<kXGroup>(3);
     };
     // One thread's waits (after one that gave up, the rest are not tried).
     auto wait = [&](bool ok, uint32_t bar, uint32_t parity) -> bool {
@@ -800,28 +925,34 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // What conv_units(k) waits for: the raw rows, the factors, X^T's buffer
     // (the rows of the chunk before last stored) and (w o X)^T's columns (the
     // last chunk's product done; the state-only walk has two sets of them).
-    auto x_ready = [&](int k) -> bool {
-        bool ok = wait(true, of(mb_dt0, k), phase(k));
+    // One lane each of a group's first four warps waits for one of these.
+    auto x_ready = [&](int k, int first) -> bool {
+        const int w = tid - first;
+        if (w == 0) return wait(true, of(mb_dt0, k), phase(k));
+        if (w == 32) return wait(true, x_bar(k), kStateOnly ? phase(k) : k & 1);
         if (kStateOnly) {
-            if (k > 1) ok = wait(ok, of(mb_sd0, k - 2), phase(k - 2));
+            if (w == 64 && k > 1) return wait(true, of(mb_sd0, k - 2), phase(k - 2));
         } else {
-            if (k > 1) ok = wait(ok, of(mb_xf0, k - 2), phase(k - 2));
-            if (k > 0) ok = wait(ok, of(mb_sd0, k - 1), phase(k - 1));
+            if (w == 64 && k > 0) return wait(true, of(mb_sd0, k - 1), phase(k - 1));
+            if (w == 96 && k > 1) return wait(true, of(mb_xf0, k - 2), phase(k - 2));
         }
-        return wait(ok, x_bar(k), kStateOnly ? phase(k) : k & 1);
+        return true;
     };
 
     if (warp >= kProducerWarp) take_registers<kRegsOne>();
     if (warp == kProducerWarp) {
         // the whole warp follows the loop, one elected lane issues: what the
-        // MMAs take then stays in uniform registers
+        // MMAs take then stays in uniform registers.  (Rolled loops of MMAs: half
+        // the instructions to fetch beside the other groups', 378 -> 364 us on 8
+        // prompts of 4096 tokens.)
         const bool issuer = elect_one();
         const uint64_t dC = tc::smem_desc(sbase + kOffC, 16, 1024);    // K-major A
         const uint64_t dBk = tc::smem_desc(sbase + kOffBh, 16, 1024);  // K-major B (G)
         const uint64_t dS = tc::smem_desc(sbase + kOffBl, 16, 1024);   // K-major B (C S^T)
         constexpr uint32_t idG = tc::idesc_bf16(128, 128, 0, 0);
         constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
-        constexpr uint32_t idY = tc::idesc_bf16(128, 64, 0, 0);
+        constexpr uint32_t idC = tc::idesc_f16(128, 128, 0, 0);
+        constexpr uint32_t idY = tc::idesc_f16(128, 64, 0, 0);
         bool ok = true;
         auto take = [&](uint32_t bar, uint32_t parity) { ok = wait(ok, bar, parity); };
         // a wait that gave up in one lane gives up in all
@@ -829,7 +960,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         auto koff = [](int ks) -> uint32_t { return (ks >> 2) * (kTile / 2) + (ks & 3) * 32; };   // K-major step
         auto issue_g = [&]() {
             if (issuer) {
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < kN / 16; ++ks)
                     tc::mma_bf16(tmem + kColG, tc::desc_add(dC, koff(ks)), tc::desc_add(dBk, koff(ks)), idG, ks > 0);
                 tc::mma_commit(mb_g);
@@ -846,7 +977,13 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         for (int k = 0; k < nk && ok; ++k) {
             const uint32_t par = k & 1;
             // (w o X)^T B: hi hi, lo hi, hi lo
-            if (kStateOnly) take(b_bar(k), phase(k));
+            if (kStateOnly) {
+                take(b_bar(k), phase(k));
+            } else {
+                take(mb_g, par);   // (G has read C: its fp16 form may come)
+                if (!all_ok()) break;
+                if (issuer) issue_c16(k);
+            }
             take(mb_s, par);
             take(of(mb_w0, k), phase(k));
             if (!all_ok()) break;
@@ -857,7 +994,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 const uint64_t dBh = tc::smem_desc(sbase + bh_off(k), kTile / 2, 1024);   // MN-major B
                 const uint64_t dBl = tc::smem_desc(sbase + bl_off(k), kTile / 2, 1024);
                 const uint32_t w = tmem + kColW - (kStateOnly && (k & 1) ? kColW : 0u);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < kQ / 16; ++ks) {
                     tc::mma_bf16_tmemA(tmem + kColS, w + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, ks > 0);
                     tc::mma_bf16_tmemA(tmem + kColS, w + 64 + 8 * ks, tc::desc_add(dBh, ks * 2048), idS, 1);
@@ -883,14 +1020,15 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
                 // Y = C S^T once the copy of S is in the B lo tile and the last
                 // chunk's rows are out of Y's columns
+                take(mb_c16, par);
                 take(mb_cs, par);
                 if (k > 0) take(mb_st, (k - 1) & 1);
                 if (!all_ok()) break;
                 tc::fence_after_sync();
                 if (issuer) {
-#pragma unroll
+#pragma unroll 1
                     for (int ks = 0; ks < kN / 16; ++ks)
-                        tc::mma_bf16(tmem + kColY, tc::desc_add(dC, koff(ks)), tc::desc_add(dS, koff(ks)), idG, ks > 0);
+                        tc::mma_bf16(tmem + kColY, tc::desc_add(dC, koff(ks)), tc::desc_add(dS, koff(ks)), idC, ks > 0);
                     tc::mma_commit(mb_yo);
                 }
                 __syncwarp();
@@ -909,7 +1047,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 // Y_h += M_h X_h
                 if (issuer) {
                     const uint64_t d0 = tc::smem_desc(sbase + xbuf(k), 16, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int ks = 0; ks < kQ / 16; ++ks) {
                         tc::mma_bf16_tmemA(tmem + kColY, tmem + kColG + 16 * ks, tc::desc_add(d0, koff(ks)), idY, 1);
                         tc::mma_bf16_tmemA(tmem + kColY + 64, tmem + kColG + 16 * ks + 8,
@@ -930,35 +1068,32 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (!ok && lane == 0) record_error(p.status, kStatusTimeout);
         __syncwarp();
     } else if (warp == kHelperWarp) {
+        // Slots 4 lane .. 4 lane + 3, one head after the other, all in registers:
+        // the first head's factors are there when their buffer comes free.
         bool ok = true;
-        for (int k = 0; k < nk; ++k) {
+        for (int k = 0; k < nk && ok; ++k) {
             const int b = k & 1;
-            if (k >= 2) {
-                if (lane == 0) ok = mbar_wait(mb_free0 + 8 * b, ((k >> 1) - 1) & 1);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
+            uint32_t b_exp = 0u, c_exp = 0u;
+            if constexpr (!kStateOnly) {
+                b_exp = *reinterpret_cast<const uint32_t *>(p.b_exp + (size_t)(wk.act + k) * kQ + 4 * lane);
+                c_exp = *reinterpret_cast<const uint32_t *>(p.c_exp + (size_t)(wk.act + k) * kQ + 4 * lane);
             }
+            // |B[s, n]| < 2^(its b_exp - 126), and for all s of the chunk
+            const uint32_t b_top = __reduce_max_sync(0xffffffffu, __vmaxu4(__vmaxu4(b_exp, b_exp >> 16), __vmaxu4(b_exp, b_exp >> 16) >> 8) & 255u);
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-            const __nv_bfloat162 *src = reinterpret_cast<const __nv_bfloat162 *>(sm + kOffDtBuf) + b * kQ + 4 * lane;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                // slots 4 lane .. 4 lane + 3: prefix sums c and, for w, suffix
-                // sums c_last - c (from the end, so that the factors that
-                // matter, near the end, come from short sums; shifted between
-                // lanes, not subtracted: a lane's own may be large)
+                const uint4 src = *(reinterpret_cast<const uint4 *>(sm + kOffDtBuf) + b * (kQ / 4) + lane);
+                const uint32_t up = h ? 0u : 16u;   // (head 0 in the lower halves)
+                const float d[4] = {__uint_as_float((src.x << up) & 0xffff0000u), __uint_as_float((src.y << up) & 0xffff0000u),
+                                    __uint_as_float((src.z << up) & 0xffff0000u), __uint_as_float((src.w << up) & 0xffff0000u)};
+                // prefix sums c and, for w, suffix sums c_last - c (from the end, so
+                // that the factors that matter, near the end, come from short sums;
+                // shifted between lanes, not subtracted: a lane's own may be large)
                 const float Aw = h ? A1 : A0;
-                const int e = (b * 2 + h) * kQ + 4 * lane;
-                float d[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = __bfloat1622float2(src[i]);
-                    d[i] = h ? f.y : f.x;
-                }
-                *reinterpret_cast<float4 *>(dts + e) = make_float4(d[0], d[1], d[2], d[3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] *= Aw;
-                float pre = (d[0] + d[1]) + (d[2] + d[3]), suf = pre;
+                const float x0 = d[0] * Aw, x1 = d[1] * Aw, x2 = d[2] * Aw, x3 = d[3] * Aw;
+                float pre = (x0 + x1) + (x2 + x3), suf = pre;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const float u = __shfl_up_sync(0xffffffffu, pre, o);
@@ -971,26 +1106,71 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 suf = __shfl_down_sync(0xffffffffu, suf, 1);
                 if (lane == 0) pre = 0.0f;
                 if (lane == 31) suf = 0.0f;
-                *reinterpret_cast<float4 *>(wgt + e) =
-                    make_float4(((suf + d[3]) + d[2]) + d[1], (suf + d[3]) + d[2], suf + d[3], suf);
-                *reinterpret_cast<float4 *>(cum + e) =
-                    make_float4(pre + d[0], (pre + d[0]) + d[1], ((pre + d[0]) + d[1]) + d[2],
-                                (((pre + d[0]) + d[1]) + d[2]) + d[3]);
-                // exp(c_last) S as S f + (S or 0): f = exp - 1 for slow decays
-                if (lane == 0)
-                    scl[b * 2 + h] = make_float2(all > -1.0f ? expm1f(all * kLn2) : exp2f(all), all);
-            }
-            __syncwarp();
-#pragma unroll 4
-            for (int i = 0; i < 2 * kQ / 32; ++i) {   // [parity][head][slot]
-                const int e = b * 2 * kQ + 32 * i + lane;
-                const float c = cum[e], d = dts[e];
-                wgt[e] = tc::exp2_approx(wgt[e]) * d;
+                const float c[4] = {pre + x0, (pre + x0) + x1, ((pre + x0) + x1) + x2, (((pre + x0) + x1) + x2) + x3};
+                float w[4] = {((suf + x3) + x2) + x1, (suf + x3) + x2, suf + x3, suf};
+                const float cR = __shfl_sync(0xffffffffu, c[3], lane | 7);   // end of the 32-slot block
+                [[maybe_unused]] float unit[4];
                 if constexpr (!kStateOnly) {
-                    fB[e] = tc::exp2_approx(cum[e | 31] - c) * d;
-                    f4[e] = tc::exp2_approx(cum[e | 3] - c) * d;
+                    // A row's unit: the power of two that takes a bound of M[t, s] to
+                    // 2^13..2^14.  |G[t, s]| <= 128 max |C_t| max |B_s|; in log2, with the
+                    // decay, over all s <= t: max(log2 |B_s| dt_s - c_s) + c_t + log2 128
+                    // |C_t|; and D.  (So a token's infinity or large value leaves the rows
+                    // before it alone.)
+                    float q = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        q = fmaxf(q, static_cast<float>(b_exp >> 8 * i & 255u) + log2_approx(d[i]) - c[i]);
+                        unit[i] = q;
+                    }
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float u = __shfl_up_sync(0xffffffffu, q, o);
+                        if (lane >= o) q = fmaxf(q, u);
+                    }
+                    q = __shfl_up_sync(0xffffffffu, q, 1);
+                    if (lane == 0) q = -INFINITY;
+                    const float lD = log2_approx(fabsf(biases[kPP + h]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = fmaxf(fmaxf(q, unit[i]) + c[i] + static_cast<float>(c_exp >> 8 * i & 255u) + (7.0f + 14.0f - 2 * 126.0f), lD);
+                        unit[i] = __int_as_float((127 + static_cast<int>(fmaxf(fminf(floorf(13.0f - e), 20.0f), -36.0f))) << 23);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = tc::exp2_approx(w[i]) * (d[i] * (1.0f / kXUnit));
+                }
+                // |what the chunk adds to the state| <= sum of w |x| |B|
+                [[maybe_unused]] float sum = (w[0] + w[1]) + (w[2] + w[3]);
+                if constexpr (!kStateOnly) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                }
+                // exp(c_last) S as S f + (S or 0): f = exp - 1 for slow decays
+                const float f = all > -1.0f ? expm1f(all * kLn2) : exp2f(all);
+                if (h == 0 && k >= 2) {
+                    if (lane == 0) ok = mbar_wait(mb_free0 + 8 * b, ((k >> 1) - 1) & 1);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                }
+                const int e = (b * 2 + h) * kQ + 4 * lane;
+                *reinterpret_cast<float4 *>(wgt + e) = make_float4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<float4 *>(cum + e) = make_float4(c[0], c[1], c[2], c[3]);
+                if (lane == 0) scl[b * 2 + h] = make_float2(f, all);
+                if constexpr (!kStateOnly) {
+                    *reinterpret_cast<float4 *>(dts + e) = make_float4(d[0], d[1], d[2], d[3]);
+                    *reinterpret_cast<float4 *>(fB + e) = make_float4(tc::exp2_approx(cR - c[0]) * d[0], tc::exp2_approx(cR - c[1]) * d[1],
+                                                                      tc::exp2_approx(cR - c[2]) * d[2], tc::exp2_approx(cR - c[3]) * d[3]);
+                    *reinterpret_cast<float4 *>(f4 + e) = make_float4(tc::exp2_approx(c[3] - c[0]) * d[0], tc::exp2_approx(c[3] - c[1]) * d[1],
+                                                                      tc::exp2_approx(c[3] - c[2]) * d[2], d[3]);
+                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(sm + kOffMUnit) + e) = make_float4(unit[0], unit[1], unit[2], unit[3]);
+                    if (lane == 0)
+                        reinterpret_cast<float *>(sm + kOffGrow)[2 * b + h] =
+                            1.01f * kXUnit * sum * __uint_as_float(min(b_top + 1u, 254u) << 23);
+                    if (h == 0) *reinterpret_cast<uint32_t *>(sm + kOffCExp + b * kQ + 4 * lane) = c_exp;
                 }
             }
+            if (!ok) break;
             if (k + 2 < nk) load_dt_async(k + 2);
             tc::mbar_arrive(mb_dt0 + 8 * b);
         }
@@ -1063,7 +1243,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll 1
                     for (int hd = 0; hd < 2; ++hd) {
                         const float *cm = c0 + hd * kQ;
-                        const float et = tc::exp2_approx(cm[row] - cm[16 * U | 31]);
+                        const float et = tc::exp2_approx(cm[row] - cm[16 * U | 31]) * cm[(kOffMUnit - kOffCum) / 4 + row];
                         const float2 et2 = make_float2(et, et);
                         const float4 *fb = reinterpret_cast<const float4 *>(cm + (kOffFB - kOffCum) / 4 + 16 * U);
                         uint32_t out[8];
@@ -1074,8 +1254,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                                                       make_float2(f.x, f.y));
                             const float2 b = tc::mul2(tc::mul2(make_float2(__uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3])), et2),
                                                       make_float2(f.z, f.w));
-                            out[2 * j] = tc::pack_bf16x2(a.x, a.y);
-                            out[2 * j + 1] = tc::pack_bf16x2(b.x, b.y);
+                            out[2 * j] = pack_f16x2(a.x, a.y);
+                            out[2 * j + 1] = pack_f16x2(b.x, b.y);
                         }
                         tc::tmem_st8_nw(gcol + 16 * U + 8 * hd, out);
                     }
@@ -1091,7 +1271,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 for (int hd = 0; hd < 2; ++hd) {
                     const float *cb = c0 + hd * kQ + 32 * quad;   // the block's
                     const float *cm = cb + 16 * h;                // the unit's
-                    const float ct = cb[row & 31], Dh = biases[kPP + hd];
+                    const float ct = cb[row & 31], unit = cb[(kOffMUnit - kOffCum) / 4 + (row & 31)], Dh = unit * biases[kPP + hd];
                     uint32_t out[8];
                     if (cb[0] - cb[31] <= 60.0f) {   // warp-uniform
                         // through 4-token blocks: exp(c_t - c_R4) exp(c_R4 - c_s);
@@ -1100,7 +1280,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         const float4 *f4h = reinterpret_cast<const float4 *>(cm + (kOffF4 - kOffCum) / 4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float rf = tc::exp2_approx(ct - cm[4 * j + 3]);
+                            const float rf = unit * tc::exp2_approx(ct - cm[4 * j + 3]);
                             const float2 rf2 = make_float2(rf, rf);
                             const float4 f = f4h[j];
                             const float2 a = tc::fma2(tc::mul2(make_float2(__uint_as_float(g[4 * j]), __uint_as_float(g[4 * j + 1])), rf2),
@@ -1109,8 +1289,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                             const float2 b = tc::fma2(tc::mul2(make_float2(__uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3])), rf2),
                                                       make_float2(f.z, f.w),
                                                       make_float2(4 * j + 2 == r ? Dh : 0.0f, 4 * j + 3 == r ? Dh : 0.0f));
-                            out[2 * j] = tc::pack_bf16x2(a.x, a.y);
-                            out[2 * j + 1] = tc::pack_bf16x2(b.x, b.y);
+                            out[2 * j] = pack_f16x2(a.x, a.y);
+                            out[2 * j + 1] = pack_f16x2(b.x, b.y);
                         }
                     } else {
                         // steep decays (or a dt that is not finite, whose
@@ -1123,11 +1303,11 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int i = 2 * j + e;
-                                const float ex = tc::exp2_approx(fminf(ct - cm[i], 0.0f));
+                                const float ex = unit * tc::exp2_approx(fminf(ct - cm[i], 0.0f));
                                 const float x = fmaf(__uint_as_float(g[i]) * ex, dh[i], i == r ? Dh : 0.0f);
                                 v[e] = i <= r ? x : 0.0f;
                             }
-                            out[j] = tc::pack_bf16x2(v[0], v[1]);
+                            out[j] = pack_f16x2(v[0], v[1]);
                         }
                     }
                     tc::tmem_st8_nw(gcol + 16 * (2 * quad + h) + 8 * hd, out);
@@ -1141,12 +1321,15 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
             }
             if (k + 1 < nk) {
-                ok = grp_and<kMGroup>(1, tid != 0 || x_ready(k + 1));
+                ok = grp_and<kMGroup>(1, x_ready(k + 1, 0));
                 if (!ok) break;
                 tc::fence_after_sync();
-                const bool bad = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h, 3 + h));
+                const bool off = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h));
                 if (tid == 0) {
-                    any_bad[2 * ((k + 1) & 1) + 1] = bad;
+                    if constexpr (!kStateOnly) {
+                        *reinterpret_cast<int *>(sm + kOffMOff) = off;
+                        tc::mbar_arrive(mb_mc);
+                    }
                     tc::mbar_arrive(of(mb_w0, k + 1));
                     if (kStateOnly) tc::mbar_arrive(of(mb_free0, k + 1));
                 }
@@ -1182,6 +1365,24 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
         }
         float dec = 0.0f;   // state-only: log2 of the walk's decay (this thread's head)
+        // Bounds of the magnitudes of this thread's row of the state and of its
+        // head's, for copy_state: found here, then carried over a chunk with what it
+        // can add (a bound that is too large only costs some of fp16's 29 octaves of
+        // full precision: 13 or so, and 4 more over the chunks between two findings).
+        float row_most = 0.0f, head_most = 0.0f;
+        auto find_bounds = [&]() {
+            uint32_t *rmax = reinterpret_cast<uint32_t *>(sm + kOffSMax);
+            uint32_t *wmax = reinterpret_cast<uint32_t *>(sm + kOffWMax) + 4 * (quad >> 1);
+            float big = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) big = max_abs3(big, st[i].x, st[i].y);
+            const uint32_t all = __reduce_max_sync(0xffffffffu, big <= kFltMax ? __float_as_uint(big) : 0u);
+            rmax[hf * kPP + prow] = __float_as_uint(big);
+            if (lane == 0) wmax[2 * hf + (quad & 1)] = all;
+            grp_sync<kYGroup>(2);
+            row_most = __uint_as_float(max(rmax[prow], rmax[kPP + prow]));
+            head_most = __uint_as_float(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+        };
         // S <- exp(c_last) S + chunk k's products
         auto next_state = [&](int k) {
             const float2 f = scl[(k & 1) * 2 + (quad >> 1)];
@@ -1201,21 +1402,45 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
             }
         };
-        // the bf16 copy of the state (operand of C S^T)
+        // the fp16 copy of the state (operand of C S^T), times a power of two
+        // whose inverse C S^T is multiplied by: one for the head, and for rows
+        // whose largest value is below 2^-18 of its (or above 2^60) their own, which
+        // (rare) takes another pass over C S^T's columns
+        float *colf = reinterpret_cast<float *>(sm + kOffColF), *headf = reinterpret_cast<float *>(sm + kOffHeadF);
+        int *rowwise = reinterpret_cast<int *>(sm + kOffRowwise);   // [head]: last chunk + 1 with such rows
+        float copy_scale = 1.0f;
+        auto choose_scale = [&](int k) {   // for chunk k's
+            const uint32_t head = min(max(__float_as_uint(head_most) >> 23, kLeastExp), kMostExp);
+            uint32_t row = __float_as_uint(row_most) >> 23;
+            const bool own = row < 255u && (row > head || (row + 18u < head && row >= kLeastExp));
+            row = own ? max(row + 120u, head) - 120u : head;
+            if (hf == 0) {
+                colf[prow] = __uint_as_float((row + 127u - head) << 23);
+                if (own) rowwise[quad >> 1] = k + 1;
+                if (lane == 0) headf[quad >> 1] = __uint_as_float(fp16_unscale_exp(head) << 23);
+            }
+            copy_scale = fp16_scale(row);
+        };
         auto copy_state = [&]() {
+            const float2 s2 = make_float2(copy_scale, copy_scale);
 #pragma unroll
             for (int pc = 0; pc < 8; ++pc) {
-                uint4 w;
-                w.x = tc::pack_bf16x2(st[4 * pc].x, st[4 * pc].y);
-                w.y = tc::pack_bf16x2(st[4 * pc + 1].x, st[4 * pc + 1].y);
-                w.z = tc::pack_bf16x2(st[4 * pc + 2].x, st[4 * pc + 2].y);
-                w.w = tc::pack_bf16x2(st[4 * pc + 3].x, st[4 * pc + 3].y);
-                *reinterpret_cast<uint4 *>(sm + kOffBl + hf * (kTile / 2) + tc::sw128(prow, pc)) = w;
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = tc::mul2(st[4 * pc + i], s2);
+                    w[i] = pack_f16x2(v.x, v.y);
+                }
+                *reinterpret_cast<uint4 *>(sm + kOffBl + hf * (kTile / 2) + tc::sw128(prow, pc)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         };
         const uint32_t ycol = tmem + lane_base + kColY + 64 * hf;
-        auto scale_rows = [&](int k) {
-            const float et = tc::exp2_approx(cum[((k & 1) * 2 + hf) * kQ + prow]);
+        // a row's factor (asked for before the wait for C S^T)
+        auto row_factor = [&](int k, float unit) {
+            return tc::exp2_approx(cum[((k & 1) * 2 + hf) * kQ + prow]) * unit * headf[hf] *
+                   __uint_as_float((uint32_t)sm[kOffCExp + (k & 1) * kQ + prow] << 23);
+        };
+        auto scale_rows = [&](int k, float et) {
             const float2 et2 = make_float2(et, et);
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -1230,38 +1455,70 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
                 tc::tmem_st16_nw(ycol + 16 * q, r);
             }
+            const bool own_x = any_bad[2 + (k & 1)] != 0;
+            if (rowwise[hf] == k + 1 || own_x) {   // (rare)
+                tc::tmem_wait_st();
+                const float *f = xfac + (k & 1) * kPP + 64 * hf;
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 4) {
+                    uint32_t r[4];
+                    tmem_ld4(ycol + c, r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * colf[64 * hf + c + i] * (own_x ? f[c + i] : 1.0f));
+                    tmem_st4_nw(ycol + c, r);
+                }
+            }
         };
         // chunk k's rows as two TMA store boxes (one per head: 128-byte rows,
         // 16-byte piece j of row t at j ^ (t & 7)) in its x buffer
-        auto stage_rows = [&](int k) {
+        auto stage_rows = [&](int k, float unit) {
             const int row = tc::no_hoist(prow);
             uint8_t *box = sm + xbuf(k) + hf * (kTile / 2);
-            const bool bad = any_bad[2 * (k & 1)] != 0 || any_bad[2 * (k & 1) + 1] != 0;   // (rare: see the top)
+            const float one = __uint_as_float(0x7f000000u - __float_as_uint(unit));   // 1 / unit
+            if (any_bad[2 + (k & 1)]) {   // (rare)
+                const float *f = xfac + (k & 1) * kPP + 64 * hf;
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 4) {
+                    uint32_t r[4];
+                    tmem_ld4(ycol + c, r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * __uint_as_float(0x7f000000u - __float_as_uint(f[c + i])));
+                    tmem_st4_nw(ycol + c, r);
+                }
+                tc::tmem_wait_st();
+            }
+            const bool bad = any_bad[k & 1] != 0;   // (rare: see the top)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t r[16];
                 tc::tmem_ld16_nw(ycol + 16 * q, r);
                 tc::tmem_wait_ld16(r);
                 if (bad) {
-                    const uint8_t *b = bad_at + (k & 1) * kParts * kPP + 64 * hf + 16 * q;
+                    const uint8_t *b = bad_at + (k & 1) * 3 * kPP + 64 * hf + 16 * q;
 #pragma unroll 1
-                    for (int part = 0; part < kParts; ++part)
+                    for (int part = 0; part < 3; ++part)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (row >= b[part * kPP + i]) r[i] = 0x7fffffffu;
                 }
 #pragma unroll
                 for (int pc = 0; pc < 2; ++pc) {
-                    uint4 w;
-                    w.x = tc::pack_bf16x2(__uint_as_float(r[8 * pc]), __uint_as_float(r[8 * pc + 1]));
-                    w.y = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 2]), __uint_as_float(r[8 * pc + 3]));
-                    w.z = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 4]), __uint_as_float(r[8 * pc + 5]));
-                    w.w = tc::pack_bf16x2(__uint_as_float(r[8 * pc + 6]), __uint_as_float(r[8 * pc + 7]));
-                    *reinterpret_cast<uint4 *>(box + tc::sw128(row, 2 * q + pc)) = w;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = tc::mul2(make_float2(__uint_as_float(r[8 * pc + 2 * i]), __uint_as_float(r[8 * pc + 2 * i + 1])),
+                                                  make_float2(one, one));
+                        w[i] = tc::pack_bf16x2(v.x, v.y);
+                    }
+                    *reinterpret_cast<uint4 *>(box + tc::sw128(row, 2 * q + pc)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
         };
         bool ok = true;
+        if constexpr (!kStateOnly) {
+            find_bounds();
+            choose_scale(0);
+        }
         if (tb == 0) tc::mbar_arrive(mb_s);   // chunk 0's products may start
         for (int k = 0; k < nk; ++k) {
             const int par = k & 1;
@@ -1283,10 +1540,18 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if (kStateOnly) tc::mbar_arrive(of(mb_free0, k));
             }
             if constexpr (!kStateOnly) {
+                // what M X's row is multiplied by (read here: from mb_free0 on it is the next but one's)
+                const float unit = kXUnit * cum[(kOffMUnit - kOffCum) / 4 + (2 * par + hf) * kQ + prow];
+                const float et = row_factor(k, unit);
+                // what is left of the state's bounds after the chunk, and what it adds
+                const float2 f = scl[par * 2 + (quad >> 1)];
+                const float keep = f.y > -1.0f ? 1.0f + f.x : f.x;
+                const float grow = reinterpret_cast<const float *>(sm + kOffGrow)[2 * par + (quad >> 1)];
+                const float more = grow * reinterpret_cast<const float *>(sm + kOffXMost)[par];
                 ok = grp_and<kYGroup>(2, tb != 0 || wait(true, mb_yo, par));
                 if (!ok) break;
                 tc::fence_after_sync();
-                scale_rows(k);
+                scale_rows(k, et);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 grp_sync<kYGroup>(2);
@@ -1294,10 +1559,19 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc::mbar_arrive(mb_ys);
                     tc::mbar_arrive(of(mb_free0, k));
                 }
+                // (here, while M X is made)
+                if ((k & 15) == 15) {
+                    find_bounds();
+                } else {
+                    // (a row's x is no larger than its head's)
+                    row_most = fmaf(row_most, keep, any_bad[2 + par] ? grow * ((65504.0f / kXUnit) * __uint_as_float(0x7f000000u - __float_as_uint(xfac[par * kPP + prow]))) : more);
+                    head_most = fmaf(head_most, keep, more);
+                }
                 ok = grp_and<kYGroup>(2, tb != 0 || wait(true, mb_e, par));
                 if (!ok) break;
                 tc::fence_after_sync();
-                stage_rows(k);
+                choose_scale(k + 1);
+                stage_rows(k, unit);
                 tc::fence_proxy_async();   // the rows, for the TMA store
                 tc::fence_before_sync();   // TMEM reads before the next product writes
                 grp_sync<kYGroup>(2);
@@ -1340,14 +1614,39 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int third = tx >> 7, pr = tx & 127;   // units 4 third .. 4 third + 3
         bool ok = true;
         for (int k = 0; k < nk; ++k) {
-            ok = grp_and<kXGroup>(3, tx != 0 || x_ready(k));
+            ok = grp_and<kXGroup>(3, x_ready(k, 32 * kXWarp));
             if (!ok) break;
             tc::fence_after_sync();
-            const bool bad = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4, third));
-            if (tx == 0) {
-                any_bad[2 * (k & 1)] = bad;
-                tc::mbar_arrive(of(mb_w0, k));
-                tc::mbar_arrive(of(mb_free0, k));
+            const bool off = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4));
+            if constexpr (kStateOnly) {
+                if (tx == 0) {
+                    tc::mbar_arrive(of(mb_w0, k));
+                    tc::mbar_arrive(of(mb_free0, k));
+                }
+            } else {
+                volatile int *again = reinterpret_cast<volatile int *>(sm + kOffAgain);
+                if (tx == 0) {
+                    // whether X^T's values, the M group's too, are finite and fit kXUnit
+                    any_bad[k & 1] = any_bad[2 + (k & 1)] = 0;
+                    reinterpret_cast<float *>(sm + kOffXMost)[k & 1] = 65504.0f / kXUnit;
+                    ok = wait(true, mb_mc, k & 1);
+                    const bool other = off || *reinterpret_cast<volatile int *>(sm + kOffMOff) != 0 ||
+                                       *reinterpret_cast<volatile int *>(sm + kOffSeen) != k + 1;
+                    if (!other) {
+                        tc::mbar_arrive(of(mb_w0, k));
+                        tc::mbar_arrive(of(mb_free0, k));
+                    }
+                    *again = other;
+                }
+                ok = grp_and<kXGroup>(3, ok);
+                if (!ok) break;
+                if (*again) {
+                    repair(k, third, pr);
+                    if (tx == 0) {
+                        tc::mbar_arrive(of(mb_w0, k));
+                        tc::mbar_arrive(of(mb_free0, k));
+                    }
+                }
             }
         }
         if (!ok && tx == 0) record_error(p.status, kStatusTimeout);
@@ -1393,7 +1692,7 @@ constexpr int kSMs = 148;
 
 struct Layout {
     int max_chunks, cut_over, seg_chunks, max_inner, max_walks, max_slots, max_cuts;
-    size_t head, walks, cuts, act, dec, state, bytes;
+    size_t head, walks, cuts, act, b_exp, c_exp, dec, state, bytes;
 };
 
 // How prompts are cut.  The pieces are as long as is best for one prompt of
@@ -1445,6 +1744,8 @@ Layout layout_of(const bimamba_dims &d)
     l.walks = take(sizeof(Walk) * (size_t)l.max_walks);
     l.cuts = take(sizeof(int4) * (size_t)l.max_cuts);
     l.act = take((size_t)l.max_chunks * kQ * kAct * 2);
+    l.b_exp = take((size_t)l.max_chunks * kQ);
+    l.c_exp = take((size_t)l.max_chunks * kQ);
     l.dec = take((size_t)l.max_slots * d.heads * 4);
     l.state = take((size_t)l.max_slots * d.heads * kP * kN * 4);
     l.bytes = at;
@@ -1494,6 +1795,8 @@ cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
     p.walks = reinterpret_cast<Walk *>(ws + l.walks);
     p.cuts = reinterpret_cast<int4 *>(ws + l.cuts);
     p.act = reinterpret_cast<__nv_bfloat16 *>(ws + l.act);
+    p.c_exp = reinterpret_cast<uint8_t *>(ws + l.c_exp);
+    p.b_exp = reinterpret_cast<uint8_t *>(ws + l.b_exp);
     p.seg_dec = reinterpret_cast<float *>(ws + l.dec);
     p.seg_state = reinterpret_cast<float *>(ws + l.state);
     p.status = q.status;

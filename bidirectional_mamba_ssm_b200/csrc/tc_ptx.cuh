@@ -49,17 +49,19 @@ __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes)
     return d + static_cast<uint64_t>(bytes >> 4);
 }
 
-// Instruction descriptor for kind::f16 with bf16 A/B and fp32 accumulate.
-// a_mn / b_mn: operand is MN-major (1) or K-major (0).
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn)
+// Instruction descriptors for kind::f16 with A and B both fp16, or both bf16,
+// and fp32 accumulate.  a_mn / b_mn: operand is MN-major (1) or K-major (0).
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
 {
     return (1u << 4)                                // D = f32
-           | (1u << 7)                              // A = bf16
-           | (1u << 10)                             // B = bf16
            | (static_cast<uint32_t>(a_mn) << 15)
            | (static_cast<uint32_t>(b_mn) << 16)
            | (static_cast<uint32_t>(N >> 3) << 17)
            | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn)
+{
+    return idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);   // A, B = bf16
 }
 
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
