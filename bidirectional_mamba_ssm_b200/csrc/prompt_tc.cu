@@ -487,7 +487,7 @@ constexpr uint32_t kOffAnyBad = kOffBad + 6 * kPP;  // int [2 parity]: there is 
 constexpr uint32_t kOffDtBuf = kOffAnyBad + 16;     // [2][128] bf16x2: dt of both heads
 constexpr uint32_t kOffTaps = kOffDtBuf + 2 * kQ * 4;   // float4 [128] conv taps, float [128] biases, float [2] D, float [3][128] halo
 constexpr uint32_t kOffMbar = kOffTaps + kPP * 20 + 8 + 3 * kPP * 4;
-constexpr uint32_t kOffTmem = kOffMbar + 176;
+constexpr uint32_t kOffTmem = kOffMbar + 192;
 constexpr uint32_t kStateRow = kN * 4 + 16;         // a row of the last state on its way out: 16-byte stores of
 static_assert(kPP * kStateRow <= 3 * kTile, "state rows");   // 8 threads' rows meet no bank twice
 
@@ -645,6 +645,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const uint32_t mb_xf0 = mb + 144;     // X^T's buffer free (the rows over it stored)
     const uint32_t mb_c16 = mb + 160;     // [k] fp16 C landed
     const uint32_t mb_mc = mb + 168;      // [k] the M group's share of X^T ready
+    const uint32_t mb_end = mb + 176;     // MMAs done, after a wait that gave up
     auto of = [](uint32_t pair, int k) { return pair + 8 * (k & 1); };
     auto phase = [](int k) -> uint32_t { return (k >> 1) & 1; };   // of a pair's barrier
     auto xbuf = [](int k) { return (k & 1) ? kOffX1 : kOffX0; };
@@ -674,6 +675,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         tc::mbar_init(mb_w0 + 8, 2);
         tc::mbar_init(mb_c16, 1);
         tc::mbar_init(mb_mc, 1);
+        tc::mbar_init(mb_end, 1);
         tc::mbar_init(mb_xf0, 1);
         tc::mbar_init(mb_xf0 + 8, 1);
         tc::mbar_init(mb_dt0, 32);
@@ -697,7 +699,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // (the state-only walk has two raw buffers)
     auto raw_off = [](int k) { return kStateOnly && (k & 1) ? kOffRaw1 : kOffRaw; };
     auto x_bar = [&](int k) { return kStateOnly && (k & 1) ? mb_cs : mb_x; };
+    struct { uint32_t x, bc, c16; } loads = {0, 0, 0};   // requests so far, of the thread that makes them
     auto issue_x = [&](int k) {
+        ++loads.x;
         tc::mbar_expect_tx(x_bar(k), kRawBytes);
         tc::tma_load_3d(sbase + raw_off(k), &tm_x, hp * kPP, first_row(k) - 3, 0, x_bar(k));
     };
@@ -713,10 +717,10 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         tc::tma_load_3d(sbase + off, &tm_bc, col, row, 0, bar);
         tc::tma_load_3d(sbase + off + kTile / 2, &tm_bc, col + 64, row, 0, bar);
     };
-    auto issue_bh = [&](int k) { issue_tile(k, bh_off(k), 0, b_bar(k)); };
-    auto issue_bl = [&](int k) { issue_tile(k, bl_off(k), kN, b_bar(k)); };
-    auto issue_c = [&](int k) { issue_tile(k, kOffC, 2 * kN, mb_bc); };
-    auto issue_c16 = [&](int k) { issue_tile(k, kOffC, 3 * kN, mb_c16); };
+    auto issue_bh = [&](int k) { ++loads.bc; issue_tile(k, bh_off(k), 0, b_bar(k)); };
+    auto issue_bl = [&](int k) { ++loads.bc; issue_tile(k, bl_off(k), kN, b_bar(k)); };
+    auto issue_c = [&](int k) { ++loads.bc; issue_tile(k, kOffC, 2 * kN, mb_bc); };
+    auto issue_c16 = [&](int k) { ++loads.c16; issue_tile(k, kOffC, 3 * kN, mb_c16); };
 
     // helper warp: dt of both heads (adjacent: one 4-byte copy per token)
     auto load_dt_async = [&](int k) {
@@ -953,6 +957,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         constexpr uint32_t idS = tc::idesc_bf16(128, 128, 0, 1);
         constexpr uint32_t idC = tc::idesc_f16(128, 128, 0, 0);
         constexpr uint32_t idY = tc::idesc_f16(128, 64, 0, 0);
+        loads.x = nk > 1 && kStateOnly ? 2 : nk > 0 ? 1 : 0;   // (in the set-up, maybe by another lane)
+        loads.bc = kStateOnly ? 2 * loads.x : 3 * loads.x;
         bool ok = true;
         auto take = [&](uint32_t bar, uint32_t parity) { ok = wait(ok, bar, parity); };
         // a wait that gave up in one lane gives up in all
@@ -1065,7 +1071,27 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
             }
         }
-        if (!ok && lane == 0) record_error(p.status, kStatusTimeout);
+        if (!ok) {
+            // what this warp has under way ends before the CTA does: shared memory
+            // and tensor memory are another's then.  (The B and C tiles of a chunk
+            // share a phase: the arrivals of those not requested yet are given to it.)
+            if (issuer) {
+                record_error(p.status, kStatusTimeout);
+                tc::mma_commit(mb_end);
+                mbar_wait(mb_end, 0);
+                if constexpr (kStateOnly) {
+                    for (uint32_t b = 0; b < 2; ++b) {
+                        if (loads.x > b) mbar_wait(x_bar(loads.x - 1 - b), phase(loads.x - 1 - b));
+                        if (loads.bc > 2 * b) mbar_wait(b_bar(loads.bc / 2 - 1 - b), phase(loads.bc / 2 - 1 - b));
+                    }
+                } else {
+                    for (; loads.bc % 3 != 0; ++loads.bc) tc::mbar_arrive(mb_bc);
+                    if (loads.x > 0) mbar_wait(mb_x, (loads.x - 1) & 1);
+                    if (loads.bc > 0) mbar_wait(mb_bc, (loads.bc / 3 - 1) & 1);
+                    if (loads.c16 > 0) mbar_wait(mb_c16, (loads.c16 - 1) & 1);
+                }
+            }
+        }
         __syncwarp();
     } else if (warp == kHelperWarp) {
         // Slots 4 lane .. 4 lane + 3, one head after the other, all in registers:
