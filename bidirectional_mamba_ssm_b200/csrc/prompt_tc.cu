@@ -132,16 +132,18 @@ struct PromptParams {
 struct Prompt {
     int begin, len, chunks;
     bool ok, bad;
+    bool back;   // its range runs backwards: others may overlap
 };
 __device__ __forceinline__ Prompt read_prompt(const PromptParams &p, int s)
 {
-    Prompt r{0, 0, 0, false, false};
+    Prompt r{0, 0, 0, false, false, false};
     if (s >= p.batch) return r;
     const int slot = p.slots[s];
     r.begin = p.cu[s];
     const int end = p.cu[s + 1];
     r.ok = slot >= 0 && slot < p.pool && r.begin >= 0 && end >= r.begin && end <= p.len;
     r.bad = !r.ok && slot >= 0;
+    r.back = end < r.begin;
     if (r.ok) {
         r.len = end - r.begin;
         r.chunks = (r.len + kQ - 1) / kQ;
@@ -273,6 +275,21 @@ prompt_prep_kernel(const PromptParams p)
             seg = nseg > 1 ? (r.chunks + nseg - 1) / nseg : r.chunks;
             if (nseg > 1) nseg = (r.chunks + seg - 1) / seg;
         };
+        // The tables hold what any prompts of p.len rows together can need.
+        // Prompts of more (ranges that overlap, which takes one that runs
+        // backwards) are reported from the first on that is too many.
+        bool back = false;
+        long long rows = 0;
+        auto fits = [&](const Prompt &r, int at) {
+            back = __syncthreads_or(back || r.back);
+            if (back) {
+                long long all;
+                const long long before = rows + block_scan((long long)r.len, &all);
+                rows += all;
+                if (before + r.len > p.len) return false;
+            }
+            return at + r.chunks <= p.max_chunks;
+        };
         auto class_of = [&](int n) { return min(3, 4 * n / (p.cut_over + 1)); };
         for (int s0 = 0; s0 < p.batch; s0 += kPrepThreads) {
             Prompt r = read_prompt(p, s0 + tid);
@@ -281,7 +298,7 @@ prompt_prep_kernel(const PromptParams p)
             const int at = chunks + block_scan(r.chunks, &all);
             // (ranges that overlap may have any number of chunks together)
             chunks = min(chunks + all, p.max_chunks + 1);
-            if (r.ok && at + r.chunks > p.max_chunks) {   // such ranges: more rows than there are
+            if (!fits(r, at) && r.ok) {
                 r.ok = false;
                 record_error(p.status, kStatusBadSlot);
             }
@@ -302,13 +319,15 @@ prompt_prep_kernel(const PromptParams p)
         int inner_at = 0, cut_at = 0;
         const int walks = next[0] + cls[0];
         chunks = 0;
+        back = false;
+        rows = 0;
         for (int s0 = 0; s0 < p.batch; s0 += kPrepThreads) {
             const int s = s0 + tid;
             Prompt r = read_prompt(p, s);
             int all, nseg, seg;
             const int at = chunks + block_scan(r.chunks, &all);
             chunks = min(chunks + all, p.max_chunks + 1);
-            if (at + r.chunks > p.max_chunks) r.ok = false;
+            if (!fits(r, at)) r.ok = false;
             shape(r, nseg, seg);
             const bool cut = r.ok && nseg > 1;
             const int wi = inner_at + block_scan(cut ? nseg - 1 : 0, &all);
@@ -1746,20 +1765,20 @@ void cut_of(long long chunks, int pairs, int &cut_over, int &seg_chunks)
     seg_chunks = (int)std::max<long long>(1, std::min<long long>(piece, cut_over));
 }
 
-// Sizes that hold for any lengths of `batch` prompts in `len` rows: a prompt
-// of L tokens has at most L / 128 + 1 chunks, and a cut one c / seg_chunks + 1
-// pieces.
+// Sizes that hold for any lengths of `batch` prompts in `len` rows.  A prompt of
+// L tokens has at most (L - 1) / 128 + 1 chunks.  Only prompts of more than
+// cut_over are cut, and one of c chunks into at most (c - 1) / seg_chunks + 1
+// pieces: their number goes by the rows, not by the other prompts.
 Layout layout_of(const bimamba_dims &d)
 {
     Layout l{};
     const long long chunks = (long long)d.len / kQ + std::min(d.batch, d.len);
     l.max_chunks = (int)chunks;
     cut_of((long long)d.len / kQ, d.heads / 2, l.cut_over, l.seg_chunks);
-    const bool cut = d.len > l.cut_over * (long long)kQ;
-    l.max_inner = cut ? (int)(chunks / l.seg_chunks) : 0;
+    l.max_cuts = (int)std::min<long long>(d.batch, d.len / (l.cut_over * (long long)kQ + 1));
+    l.max_inner = l.max_cuts > 0 ? d.len / kQ / l.seg_chunks : 0;
     l.max_walks = l.max_inner + d.batch;
-    l.max_slots = 2 * l.max_inner;
-    l.max_cuts = l.max_chunks / (l.cut_over + 1);
+    l.max_slots = l.max_inner + l.max_cuts;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
