@@ -470,8 +470,8 @@ def bimamba_prompt_workspace_bytes(dims: Dims) -> int:
 
 
 def new_prompt_workspace(xbc, *, batch, heads, headdim, d_state) -> torch.Tensor:
-    """Workspace for bimamba_prompt_scan on packed rows like xbc's, for up to
-    `batch` prompts."""
+    """Workspace for bimamba_prompt_scan on packed rows like xbc's or fewer,
+    for up to `batch` prompts."""
     n = bimamba_prompt_workspace_bytes(make_dims(batch, xbc.shape[0], heads, headdim, d_state,
                                                  _dtype_code(xbc)))
     return torch.empty(max(256, n), dtype=torch.uint8, device=xbc.device)

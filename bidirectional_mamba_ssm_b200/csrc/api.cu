@@ -494,12 +494,18 @@ static int check_causal(const bimamba_dims *d, const void *xbc, const void *dt, 
     return any_output_overlaps(r, 4, 13) ? BIMAMBA_ERR_INVALID : BIMAMBA_OK;
 }
 
+// What a call needs (fewer: and any call of fewer rows or prompts); 256 bytes
+// at least: a workspace is always wanted.
+static size_t prompt_ws_bytes(const bimamba_dims &d, bool fewer)
+{
+    const size_t n = prompt_tc_supported(d) ? prompt_tc_ws_bytes(d, fewer) : prompt_seq_ws_bytes(d);
+    return (n + 511) & ~(size_t)255;
+}
+
 size_t bimamba_prompt_workspace_bytes(const bimamba_dims *d)
 {
     if (check_dims(d) != BIMAMBA_OK || d->len > (1 << 30)) return 0;
-    // (256 bytes at least: a workspace is always wanted)
-    const size_t n = prompt_tc_supported(*d) ? prompt_tc_ws_bytes(*d) : prompt_seq_ws_bytes(*d);
-    return (n + 511) & ~(size_t)255;
+    return prompt_ws_bytes(*d, true);
 }
 
 int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, const float *A,
@@ -514,7 +520,7 @@ int bimamba_prompt_scan(const bimamba_dims *d, const void *xbc, const void *dt, 
     if (d->batch == 0) return BIMAMBA_OK;
     if (!cu_seqlens) return BIMAMBA_ERR_INVALID;
     st = check_causal(d, xbc, dt, A, D, conv_w, conv_b, cu_seqlens, state_pool, tail_pool, pool_size,
-                      slots, resume, y, workspace, workspace_bytes, bimamba_prompt_workspace_bytes(d));
+                      slots, resume, y, workspace, workspace_bytes, prompt_ws_bytes(*d, false));
     if (st != BIMAMBA_OK) return st;
     PromptProblem q{};
     q.dims = *d;

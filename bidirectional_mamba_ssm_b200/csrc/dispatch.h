@@ -146,7 +146,7 @@ template <typename T>
 cudaError_t launch_prompt_seq(const PromptProblem &q, cudaStream_t stream);
 size_t prompt_seq_ws_bytes(const bimamba_dims &d);
 bool prompt_tc_supported(const bimamba_dims &d);   // bf16, headdim 64, d_state 128, even heads
-size_t prompt_tc_ws_bytes(const bimamba_dims &d);
+size_t prompt_tc_ws_bytes(const bimamba_dims &d, bool fewer);   // fewer: and of calls of fewer rows
 cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream);
 
 // one token per cached stream

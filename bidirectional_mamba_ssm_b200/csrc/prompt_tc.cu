@@ -1769,14 +1769,32 @@ void cut_of(long long chunks, int pairs, int &cut_over, int &seg_chunks)
 // L tokens has at most (L - 1) / 128 + 1 chunks.  Only prompts of more than
 // cut_over are cut, and one of c chunks into at most (c - 1) / seg_chunks + 1
 // pieces: their number goes by the rows, not by the other prompts.
-Layout layout_of(const bimamba_dims &d)
+// `fewer`: that fit calls of fewer rows, too, for which the rule may cut more
+// (14976 rows in 64 heads take 6 pieces, 15104 take 4).  Every count of chunks
+// is tried up to kTried (a millisecond, in the size query alone); of more, a
+// piece has a 16th of the rows at least and a prompt that is cut 1.5 of that,
+// so that there are at most 16 and 10.
+Layout layout_of(const bimamba_dims &d, bool fewer)
 {
     Layout l{};
     const long long chunks = (long long)d.len / kQ + std::min(d.batch, d.len);
     l.max_chunks = (int)chunks;
-    cut_of((long long)d.len / kQ, d.heads / 2, l.cut_over, l.seg_chunks);
-    l.max_cuts = (int)std::min<long long>(d.batch, d.len / (l.cut_over * (long long)kQ + 1));
-    l.max_inner = l.max_cuts > 0 ? d.len / kQ / l.seg_chunks : 0;
+    auto cuts_of = [&](long long rows) {
+        cut_of(rows / kQ, d.heads / 2, l.cut_over, l.seg_chunks);
+        const int cuts = (int)std::min<long long>(d.batch, rows / (l.cut_over * (long long)kQ + 1));
+        l.max_cuts = std::max(l.max_cuts, cuts);
+        if (cuts > 0) l.max_inner = std::max(l.max_inner, (int)(rows / kQ / l.seg_chunks));
+    };
+    if (fewer) {
+        constexpr int kTried = 4096;
+        for (int c = std::min(d.len / kQ, kTried); c >= 0; --c) cuts_of((long long)c * kQ + kQ - 1);
+        if (d.len / kQ > kTried) {
+            l.max_cuts = std::max(l.max_cuts, std::min(d.batch, 10));
+            l.max_inner = std::max(l.max_inner, 16);
+        }
+    } else {
+        cuts_of(d.len);
+    }
     l.max_walks = l.max_inner + d.batch;
     l.max_slots = l.max_inner + l.max_cuts;
     size_t at = 0;
@@ -1821,12 +1839,12 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, ui
 
 }  // namespace
 
-size_t prompt_tc_ws_bytes(const bimamba_dims &d) { return layout_of(d).bytes; }
+size_t prompt_tc_ws_bytes(const bimamba_dims &d, bool fewer) { return layout_of(d, fewer).bytes; }
 
 cudaError_t launch_prompt_tc(const PromptProblem &q, cudaStream_t stream)
 {
     const bimamba_dims &d = q.dims;
-    const Layout l = layout_of(d);
+    const Layout l = layout_of(d, false);
     char *ws = static_cast<char *>(q.workspace);
     PromptParams p{};
     p.xbc = static_cast<const __nv_bfloat16 *>(q.xbc);

@@ -379,8 +379,10 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
  *                resumes leaves its entry as it is, one that does not zeroes it.
  *   y          : (len, H*P) dtype
  *   workspace  : bimamba_prompt_workspace_bytes(d) bytes, 256-byte aligned,
- *                no clearing needed.  Calls that share one (two graphs, too)
- *                must not run concurrently.
+ *                no clearing needed.  The size does not fall as len or batch
+ *                grow: one made for the largest serves every smaller call of
+ *                the same heads, headdim, d_state and dtype.  Calls that share
+ *                one (two graphs, too) must not run concurrently.
  * What only the device knows is checked there: a prompt whose slot is
  * outside [0, pool_size) or is another prompt's too, or whose rows are not a
  * range inside [0, len), is skipped (y and the pool untouched) and makes

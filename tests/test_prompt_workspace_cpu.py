@@ -24,3 +24,17 @@ def test_short_prompts_need_no_segments(lib, heads, prompts, rows):
     chunks = rows // 128 + min(prompts, rows)
     segments = 48 * (heads * 64 * 128 * 4 + 256)
     assert _bytes(lib, heads, prompts, rows) <= chunks * 128 * 1026 + 64 * (prompts + 48) + segments + 4096
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("heads", [2, 16, 48, 64, 96])
+def test_a_larger_call_needs_no_less(lib, heads, dtype):
+    """Rows and prompts each up: never fewer bytes (a workspace made for the
+    largest call serves all)."""
+    sizes = [[_bytes(lib, heads, prompts, rows, dtype) for rows in
+              [*range(0, 40000, 331), 65536, 100000, 524288 + 127, 524288 + 128, 1 << 20, 3 << 20]]
+             for prompts in (1, 2, 5, 8, 11, 64)]
+    for row in sizes:
+        assert all(a <= b for a, b in zip(row, row[1:]))
+    for a, b in zip(sizes, sizes[1:]):
+        assert all(p <= q for p, q in zip(a, b))
