@@ -45,7 +45,7 @@ token_step_kernel(const StepProblem q)
     constexpr int kPer = kRowVecs / kLanes;               // float4s of a row per thread (N = 256: 2)
     constexpr int kRowsPass = kStepThreads / kLanes;      // state rows per pass
     constexpr int kPasses = kStepLoads / kPer;            // passes whose loads are in flight together
-    __shared__ float act[128 + 2 * N];                    // x (this head) | B | C
+    __shared__ __align__(16) float act[128 + 2 * N];      // x (this head) | B | C; B and C read as float4
     __shared__ int last_reader;
 
     const int h = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
