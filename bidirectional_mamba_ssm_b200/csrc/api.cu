@@ -64,11 +64,11 @@ static int check_dims(const bimamba_dims *d)
     return BIMAMBA_OK;
 }
 
-// Whether [a, a + an) and [b, b + bn) share a byte (null ranges share none).
+// Whether [a, a + an) and [b, b + bn) share a byte (null and empty ranges share none).
 static bool overlap(const void *a, size_t an, const void *b, size_t bn)
 {
     const char *p = static_cast<const char *>(a), *q = static_cast<const char *>(b);
-    return p && q && p < q + bn && q < p + an;
+    return p && q && an > 0 && bn > 0 && p < q + bn && q < p + an;
 }
 
 // Whether any of the `nout` first ranges overlaps another of the `n`.
