@@ -895,32 +895,47 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // X^T of chunk k once more (rare), by the X group, all 16 units of 8 tokens
     // from the raw rows: values that are not finite as zeros, the first such
     // token of a channel noted in bad_at; a channel whose largest value is past
-    // fp16's range or near its small end times a power of two of its own.
+    // fp16's range or near its small end times a power of two of its own.  (8
+    // prompts of 4096 tokens whose every chunk has activations past 2^8: 835 us
+    // for 374.)
     float *xfac = reinterpret_cast<float *>(sm + kOffXFac);
     auto repair = [&](int k, int third, int pr) {
         const int par = k & 1;
         const float4 w4 = taps[pr];
+        const float bias = biases[pr];
         const int rows = tokens(k) + 3;
         const uint16_t *raw = reinterpret_cast<const uint16_t *>(sm + raw_off(k)) + pr;
         auto row = [&](int t) -> float {   // as in conv_units
-            return t < 3 && k == 0 && starts ? halo[t * kPP + pr]
-                 : t < rows ? __uint_as_float(static_cast<uint32_t>(raw[t * kPP]) << 16) : 0.0f;
+            return t < rows ? __uint_as_float(static_cast<uint32_t>(raw[t * kPP]) << 16) : 0.0f;
         };
-        auto x = [&](int i) -> float {   // of token i, in the same steps as there
-            const float a = fmaf(w4.w, row(i + 3), fmaf(w4.y, row(i + 1), fmaf(w4.z, row(i + 2), fmaf(w4.x, row(i), biases[pr]))));
-            return silu2<kXUnit>(make_float2(a, a)).x;
+        // this thread's third of the tokens, in order: f(token, activation), in
+        // the same steps as there
+        auto each = [&](auto f) {
+            constexpr int kThird = (kQ + 2) / 3;
+            const int i0 = kThird * third, i1 = min(i0 + kThird, kQ);
+            const bool in_halo = i0 == 0 && k == 0 && starts;
+            float v0 = in_halo ? halo[pr] : row(i0), v1 = in_halo ? halo[kPP + pr] : row(i0 + 1);
+            float v2 = in_halo ? halo[2 * kPP + pr] : row(i0 + 2);
+#pragma unroll 4
+            for (int i = i0; i < i1; ++i) {
+                const float v3 = row(i + 3);
+                const float a = fmaf(w4.w, v3, fmaf(w4.y, v1, fmaf(w4.z, v2, fmaf(w4.x, v0, bias))));
+                f(i, silu2<kXUnit>(make_float2(a, a)).x);
+                v0 = v1;
+                v1 = v2;
+                v2 = v3;
+            }
         };
-        uint32_t *most = reinterpret_cast<uint32_t *>(xfac + par * kPP + pr);   // (zeros until then)
+        uint32_t *most = reinterpret_cast<uint32_t *>(xfac + par * kPP + pr);   // (of the channel, until its factor is known)
         float big = 0.0f;
         int at = kQ;
         if (third == 0) *most = 0u;
         grp_sync<kXGroup>(3);
-#pragma unroll 1
-        for (int i = third; i < kQ; i += 3) {
-            const float v = fabsf(x(i));
+        each([&](int i, float x) {
+            const float v = fabsf(x);
             if (v <= kFltMax) big = fmaxf(big, v);
             else at = min(at, i);
-        }
+        });
         bad_at[(par * 3 + third) * kPP + pr] = (uint8_t)at;
         if (at < kQ) any_bad[par] = 1;
         atomicMax(most, __float_as_uint(big));
@@ -933,11 +948,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         grp_sync<kXGroup>(3);
         if (third == 0) xfac[par * kPP + pr] = f;
         __half *xt = reinterpret_cast<__half *>(sm + xbuf(k));
-#pragma unroll 1
-        for (int i = third; i < kQ; i += 3) {
-            const float v = x(i);
-            xt[(i >> 6) * (kTile / 4) + tc::sw128(pr, i >> 3 & 7) / 2 + (i & 7)] = __float2half_rn(fabsf(v) <= kFltMax ? f * v : 0.0f);
-        }
+        each([&](int i, float x) {
+            xt[(i >> 6) * (kTile / 4) + tc::sw128(pr, i >> 3 & 7) / 2 + (i & 7)] = __float2half_rn(fabsf(x) <= kFltMax ? f * x : 0.0f);
+        });
         tc::fence_proxy_async();
         grp_sync<kXGroup>(3);
     };
