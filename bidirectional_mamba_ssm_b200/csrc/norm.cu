@@ -11,10 +11,10 @@
 //     dg = sum over rows of dy z,   db = sum over rows of dy.
 //
 // Bound by HBM: every activation is read or written once, everything else
-// stays in registers.  A row belongs to `kWarps` warps, each thread holding
-// `kVec` 16-byte-per-8-element vectors of it.  32768 x 2048 bf16: the forward
-// with a residual and the backward with dsum 88 and 98 us, where the bytes
-// take 82 at the card's copy rate.
+// stays in registers.  A row belongs to `kWarps` warps, each thread holding up
+// to kFwdVec (backward: kBwdVec) vectors of 8 of its elements.  32768 x 2048
+// bf16: the forward with a residual and the backward with dsum 89 and 99 us,
+// where the bytes take 82 at the card's copy rate.
 #include "common.cuh"
 #include "dispatch.h"
 #include "tc_ptx.cuh"

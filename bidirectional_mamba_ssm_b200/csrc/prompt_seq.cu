@@ -1,6 +1,7 @@
 // prompt_seq.cu -- the causal mixer core over packed ragged prompts on the
-// CUDA cores, in fp32: fp32 activations (bf16 operands could not hold their
-// bound) and the head shapes without a tensor-core kernel.
+// CUDA cores, in fp32: fp32 activations (the tensor-core kernel's y is made for
+// bf16; its 16-bit operands would need two halves each throughout, as its state's
+// have) and the head shapes without a tensor-core kernel.
 //
 // Operation (Mamba-2 recurrence, d_conv = 4; the cache entry of "Fixed state,
 // long reach: constant-size caches in large-scale block diffusion"), for each

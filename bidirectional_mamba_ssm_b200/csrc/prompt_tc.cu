@@ -44,8 +44,8 @@
 //   1. plan + conv of B and C: per 128-token chunk the operand rows
 //      [B hi | B lo | C | C in fp16] and their exponents (zeros behind the
 //      prompt's end, so that a neighbour never enters a product), and, by one
-//      CTA, the table of walks.  All of
-//      it latency (7 us for 68 chunks of 11 prompts): short loops, few scans.
+//      CTA, the table of walks.  All of it latency (10 us for 74 chunks of 11
+//      prompts, alone): short loops, few scans.
 //   2. only where a prompt may be long against the GPU's share of the work
 //      (segment_chunks): prompts above that are cut into equal segments; a
 //      state-only walk of each segment but the last, then
@@ -63,10 +63,11 @@
 // of G or M X, or freeing (w o X)^T a quarter at a time, gains nothing: the
 // conv, M and the row work then wait for the same issue slots.  A walk's
 // beginning and end take about 13 us besides.
-// Measured, 64 heads, calls one after another on the same buffers: 8 prompts of
-// 4096 tokens 374 us, one of 32768 534, 11 ragged ones of 8126 in all 136, 37
-// tokens 22.5 (18 of them the host's call).  (With bf16 operands throughout 361,
-// 540, 127 and 21.)
+// Measured, 64 heads, calls one after another on the same buffers, three cards:
+// 8 prompts of 4096 tokens 374..386 us, one of 32768 534..552, 11 ragged ones of
+// 8126 in all 136..139, 37 tokens 22.5 (18 of them the host's call).  On one card
+// in turn with the form whose operands were all bf16: 364 for 341, 506 for 504,
+// 137 for 129.
 #include "common.cuh"
 #include "dispatch.h"
 #include "tc_ptx.cuh"
@@ -897,7 +898,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // token of a channel noted in bad_at; a channel whose largest value is past
     // fp16's range or near its small end times a power of two of its own.  (8
     // prompts of 4096 tokens whose every chunk has activations past 2^8: 835 us
-    // for 374.)
+    // for 375.)
     float *xfac = reinterpret_cast<float *>(sm + kOffXFac);
     auto repair = [&](int k, int third, int pr) {
         const int par = k & 1;
@@ -1760,8 +1761,9 @@ struct Layout {
 // longer than these do: a piece's state-only walk, three chunks' time for two
 // more launches, and the GPU's share of the call (a fifth added: walks do not
 // fill it evenly).  1311, 1, 640, 129, 0, 2777, 63, 1024, 517, 1536 and 128
-// tokens in 64 heads: 150 us, with the 2777 in two pieces 178 (both faster
-// since).
+// tokens in 64 heads: 138 us, with the 2777 in two pieces 166.  (The host knows
+// the rows that there is room for, not the prompts' lengths: a call with room for
+// many rows does not cut a prompt that few of them make.)
 void cut_of(long long chunks, int pairs, int &cut_over, int &seg_chunks)
 {
     const long long share = (chunks * pairs + kSMs - 1) / kSMs;

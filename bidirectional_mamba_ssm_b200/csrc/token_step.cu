@@ -12,12 +12,15 @@
 // and is nearly all of the traffic (per 64 x 128 head 64 KB, against ~6 KB of
 // conv inputs that its CTA reads mostly from L2).  One CTA per (row, head),
 // so that a single row already spreads over many SMs; every thread requests
-// its whole share of the state before anything else, and the conv of the
-// head's x and the row's B and C (recomputed by every head: they are small,
-// and a launch of their own would cost more than the reads) runs under those
-// loads.
-// 64 heads of 64 x 128: 256 rows fp32 184 us (bytes 170), 32 rows bf16 25
-// (21), one row 13, the host's call.
+// the first kStepLoads of its vectors of the state before anything else (at
+// 64 x 128 half of them: the others follow the first half's update), and the
+// conv of the head's x and the row's B and C (recomputed by every head: they
+// are small, and a launch of their own would cost more than the reads) runs
+// under those loads.
+// 64 heads of 64 x 128, calls one after another on the same buffers: 256 rows
+// fp32 194 us (bytes 170), 32 rows bf16 29 (21; 2048 CTAs, 740 at a time: what
+// is left is the overlap of a CTA's stores with its successor's loads), one row
+// 12, the host's call.
 #include "common.cuh"
 #include "dispatch.h"
 
