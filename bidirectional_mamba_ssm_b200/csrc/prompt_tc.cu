@@ -494,11 +494,13 @@ constexpr uint32_t kOffCExp = kOffSMax + 8 * kPP;   // u8 [2 parity][128]: c_exp
 constexpr uint32_t kOffMUnit = kOffCExp + 2 * kQ;   // float [2 parity][2 head][128]: what M's rows are multiplied by
 constexpr uint32_t kOffXFac = kOffMUnit + kFac;     // float [2 parity][128]: what channels of X^T are multiplied by besides, see repair
 constexpr uint32_t kOffGrow = kOffXFac + 2 * kPP * 4;   // float [2 parity][2 head]: what the chunk adds to the state for |x| = 1 at most
-constexpr uint32_t kOffXMost = kOffGrow + 16;       // float [2 parity]: bound of the finite |x|
-constexpr uint32_t kOffSeen = kOffXMost + 8;        // int: last chunk + 1 with a value from 2^-12 on in X^T
-constexpr uint32_t kOffMOff = kOffSeen + 4;         // int: the M group's share of X^T is not as it should be
+constexpr uint32_t kOffXRow = kOffGrow + 16;        // fp16 [2 parity][part][128]: largest of X^T's magnitudes, of a thread
+constexpr int kParts = 5;                           // of a chunk's units: 3 x 4 (X group), 2 x 2 (M group)
+constexpr uint32_t kOffXHead = kOffXRow + 2 * kParts * kPP * 2;   // u32 [2 parity][2 head]: the same of a head, zeros between
+constexpr uint32_t kOffXMost = kOffXHead + 16;      // float [2 parity][2 head]: bound of the head's finite |x|
+constexpr uint32_t kOffMOff = kOffXMost + 16;        // int: the M group's share of X^T is not as it should be
 constexpr uint32_t kOffAgain = kOffMOff + 4;        // int: X^T has to be made again
-constexpr uint32_t kOffWMax = kOffAgain + 16;       // float [2 head][4]: largest of a Y warp's state values
+constexpr uint32_t kOffWMax = kOffAgain + 12;       // float [2 head][4]: largest of a Y warp's state values
 constexpr uint32_t kOffHeadF = kOffWMax + 32;       // float [2 head]: what takes the state copy's scale from C S^T
 constexpr uint32_t kOffRowwise = kOffHeadF + 8;     // int [2 head], see choose_scale
 constexpr uint32_t kOffScale = kOffRowwise + 8;     // float2 [2 parity][2 head]: see next_state
@@ -513,7 +515,7 @@ static_assert(kPP * kStateRow <= 3 * kTile, "state rows");   // 8 threads' rows 
 
 constexpr uint32_t kSmemBytes = kOffTmem + 16 + 1024;   // + alignment slack
 static_assert(kOffRaw % 1024 == 0 && kOffFac % 16 == 0 && kOffColF % 16 == 0 && kOffCExp % 4 == 0 && kOffMUnit % 16 == 0 &&
-                  kOffXFac % 4 == 0 && kOffWMax % 16 == 0 &&
+                  kOffXFac % 4 == 0 && kOffXRow % 4 == 0 && kOffXHead % 4 == 0 && kOffWMax % 16 == 0 &&
                   kOffScale % 8 == 0 && kOffAnyBad % 4 == 0 && kOffDtBuf % 16 == 0 && kOffTaps % 16 == 0 && kOffMbar % 8 == 0 &&
                   kOffTmem % 4 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 
@@ -782,7 +784,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         biases[tid] = kXUnit * my_bias;
     }
     if (tid < 2) biases[kPP + tid] = p.D[2 * hp + tid];
-    if (tid == 0) *reinterpret_cast<int *>(sm + kOffSeen) = 0;
+    if (tid < 4) reinterpret_cast<uint32_t *>(sm + kOffXHead)[tid] = 0u;
     if (tid < 2) reinterpret_cast<int *>(sm + kOffRowwise)[tid] = 0;
     // the 3 tokens before the walk's first chunk where they are not in the raw
     // tile: the prompt's entry's tail, or zeros
@@ -815,7 +817,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // memory (lane = channel, so that a thread's tokens are consecutive:
     // 16-byte stores of X^T, and the A operand's layout).  Returns whether a
     // value is not finite, in X^T's fp16 with kXUnit at least.
-    auto conv_units = [&](int k, int pr, int ua, int ub) -> bool {
+    auto conv_units = [&](int k, int pr, int ua, int ub, int part) -> bool {
         const int par = k & 1;
         const float4 w4 = taps[pr];
         const float bias = biases[pr];
@@ -840,8 +842,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const float2 wa = make_float2(w4.x, w4.x), wc = make_float2(w4.z, w4.z), b2 = make_float2(bias, bias);
         // unit u's 16 bytes of X^T's row
         auto piece = [&](int u) { return (u >> 3) * (kTile / 2) + tc::sw128(pr, u & 7); };
-        [[maybe_unused]] __half2 check = __float2half2_rn(0.0f);   // NaN once a value is not finite in fp16
-        [[maybe_unused]] uint32_t bits = 0u;                       // of all of them
+        [[maybe_unused]] uint32_t largest = 0u;   // of X^T's magnitudes, the words of an fp16 pair
 #pragma unroll 2
         for (int u = ua; u < ub; ++u) {
             float v[11];
@@ -872,8 +873,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 const float2 x = silu2<kXUnit>(a);
                 if constexpr (!kStateOnly) {
                     xp[j] = pack_f16x2(x.x, x.y);
-                    check = __hfma2(*reinterpret_cast<const __half2 *>(&xp[j]), __float2half2_rn(0.0f), check);
-                    bits |= xp[j];
+                    if (j & 1) largest = __vimax3_u16x2(largest, xp[j - 1] & 0x7fff7fffu, xp[j] & 0x7fff7fffu);
                 }
                 const float2 w = j == 0 ? make_float2(w01.x, w01.y) : j == 1 ? make_float2(w01.z, w01.w)
                                : j == 2 ? make_float2(w23.x, w23.y) : make_float2(w23.z, w23.w);
@@ -885,13 +885,15 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             tmem_st4_nw(wcol + 64 + 4 * u, lo);
         }
         if constexpr (!kStateOnly) {
-            const bool seen = ((bits | bits >> 16) & 0x7c00u) >= 0x0c00u;   // (2^-12)
-            if (__any_sync(0xffffffffu, seen) && lane == 0) *reinterpret_cast<volatile int *>(sm + kOffSeen) = k + 1;
+            largest = max(largest >> 16, largest & 0xffffu);
+            reinterpret_cast<uint16_t *>(sm + kOffXRow)[(par * kParts + part) * kPP + pr] = (uint16_t)largest;
+            const uint32_t all = __reduce_max_sync(0xffffffffu, largest);
+            if (lane == 0) atomicMax(reinterpret_cast<uint32_t *>(sm + kOffXHead) + 2 * par + (pr >> 6), all);
         }
         tc::tmem_wait_st();
         if constexpr (!kStateOnly) tc::fence_proxy_async();   // X^T, for the tensor core
         tc::fence_before_sync();
-        return !(__low2float(check) == 0.0f && __high2float(check) == 0.0f);
+        return !kStateOnly && largest >= 0x7c00u;
     };
     // X^T of chunk k once more (rare), by the X group, all 16 units of 8 tokens
     // from the raw rows: values that are not finite as zeros, the first such
@@ -940,7 +942,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         bad_at[(par * 3 + third) * kPP + pr] = (uint8_t)at;
         if (at < kQ) any_bad[par] = 1;
         atomicMax(most, __float_as_uint(big));
-        atomicMax(reinterpret_cast<uint32_t *>(sm + kOffXMost) + par, __float_as_uint(big * (1.0f / kXUnit)));
+        atomicMax(reinterpret_cast<uint32_t *>(sm + kOffXMost) + 2 * par + (pr >> 6), __float_as_uint(big * (1.0f / kXUnit)));
         grp_sync<kXGroup>(3);
         big = __uint_as_float(*most);
         const bool own = big >= 65504.0f || (big < 0x1p-12f && big != 0.0f);
@@ -1178,7 +1180,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     float q = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        q = fmaxf(q, static_cast<float>(b_exp >> 8 * i & 255u) + log2_approx(d[i]) - c[i]);
+                        q = fmaxf(q, static_cast<float>(b_exp >> 8 * i & 255u) + log2_approx(fabsf(d[i])) - c[i]);
                         unit[i] = q;
                     }
 #pragma unroll
@@ -1200,7 +1202,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     w[i] = tc::exp2_approx(w[i]) * (d[i] * (1.0f / kXUnit));
                 }
                 // |what the chunk adds to the state| <= sum of w |x| |B|
-                [[maybe_unused]] float sum = (w[0] + w[1]) + (w[2] + w[3]);
+                [[maybe_unused]] float sum = (fabsf(w[0]) + fabsf(w[1])) + (fabsf(w[2]) + fabsf(w[3]));
                 if constexpr (!kStateOnly) {
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -1383,7 +1385,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 ok = grp_and<kMGroup>(1, x_ready(k + 1, 0));
                 if (!ok) break;
                 tc::fence_after_sync();
-                const bool off = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h));
+                const bool off = grp_or<kMGroup>(1, conv_units(k + 1, row, 12 + 2 * h, 14 + 2 * h, 3 + h));
                 if (tid == 0) {
                     if constexpr (!kStateOnly) {
                         *reinterpret_cast<int *>(sm + kOffMOff) = off;
@@ -1426,8 +1428,9 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         float dec = 0.0f;   // state-only: log2 of the walk's decay (this thread's head)
         // Bounds of the magnitudes of this thread's row of the state and of its
         // head's, for copy_state: found here, then carried over a chunk with what it
-        // can add (a bound that is too large only costs some of fp16's 29 octaves of
-        // full precision: 13 or so, and 4 more over the chunks between two findings).
+        // can add: sum of w, times the largest |B|, times the row's largest |x| (a
+        // bound that is too large only costs some of fp16's 29 octaves of full
+        // precision: 8 or so, and 2 more over the chunks between two findings).
         float row_most = 0.0f, head_most = 0.0f;
         auto find_bounds = [&]() {
             uint32_t *rmax = reinterpret_cast<uint32_t *>(sm + kOffSMax);
@@ -1463,7 +1466,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         };
         // the fp16 copy of the state (operand of C S^T), times a power of two
         // whose inverse C S^T is multiplied by: one for the head, and for rows
-        // whose largest value is below 2^-18 of its (or above 2^60) their own, which
+        // whose largest value is below 2^-16 of its (or above 2^60) their own, which
         // (rare) takes another pass over C S^T's columns
         float *colf = reinterpret_cast<float *>(sm + kOffColF), *headf = reinterpret_cast<float *>(sm + kOffHeadF);
         int *rowwise = reinterpret_cast<int *>(sm + kOffRowwise);   // [head]: last chunk + 1 with such rows
@@ -1471,7 +1474,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         auto choose_scale = [&](int k) {   // for chunk k's
             const uint32_t head = min(max(__float_as_uint(head_most) >> 23, kLeastExp), kMostExp);
             uint32_t row = __float_as_uint(row_most) >> 23;
-            const bool own = row < 255u && (row > head || (row + 18u < head && row >= kLeastExp));
+            const bool own = row < 255u && (row > head || (row + 16u < head && row >= kLeastExp));
             row = own ? max(row + 120u, head) - 120u : head;
             if (hf == 0) {
                 colf[prow] = __uint_as_float((row + 127u - head) << 23);
@@ -1606,7 +1609,12 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 const float2 f = scl[par * 2 + (quad >> 1)];
                 const float keep = f.y > -1.0f ? 1.0f + f.x : f.x;
                 const float grow = reinterpret_cast<const float *>(sm + kOffGrow)[2 * par + (quad >> 1)];
-                const float more = grow * reinterpret_cast<const float *>(sm + kOffXMost)[par];
+                const float more = grow * reinterpret_cast<const float *>(sm + kOffXMost)[2 * par + (quad >> 1)];
+                const uint16_t *xr = reinterpret_cast<const uint16_t *>(sm + kOffXRow) + par * kParts * kPP + prow;
+                const uint32_t x_row = max(max(max((uint32_t)xr[0], (uint32_t)xr[kPP]), (uint32_t)xr[2 * kPP]), max((uint32_t)xr[3 * kPP], (uint32_t)xr[4 * kPP]));
+                float more_row = grow * ((1.0f / kXUnit) * __half2float(__ushort_as_half((uint16_t)min(x_row, 0x7bffu))));
+                if (any_bad[2 + par] && xfac[par * kPP + prow] != 1.0f)   // (rare)
+                    more_row = grow * ((65504.0f / kXUnit) * __uint_as_float(0x7f000000u - __float_as_uint(xfac[par * kPP + prow])));
                 ok = grp_and<kYGroup>(2, tb != 0 || wait(true, mb_yo, par));
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -1622,8 +1630,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 if ((k & 15) == 15) {
                     find_bounds();
                 } else {
-                    // (a row's x is no larger than its head's)
-                    row_most = fmaf(row_most, keep, any_bad[2 + par] ? grow * ((65504.0f / kXUnit) * __uint_as_float(0x7f000000u - __float_as_uint(xfac[par * kPP + prow]))) : more);
+                    row_most = fmaf(row_most, keep, more_row);
                     head_most = fmaf(head_most, keep, more);
                 }
                 ok = grp_and<kYGroup>(2, tb != 0 || wait(true, mb_e, par));
@@ -1676,7 +1683,7 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             ok = grp_and<kXGroup>(3, x_ready(k, 32 * kXWarp));
             if (!ok) break;
             tc::fence_after_sync();
-            const bool off = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4));
+            const bool off = grp_or<kXGroup>(3, conv_units(k, pr, 4 * third, 4 * third + 4, third));
             if constexpr (kStateOnly) {
                 if (tx == 0) {
                     tc::mbar_arrive(of(mb_w0, k));
@@ -1686,11 +1693,16 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 volatile int *again = reinterpret_cast<volatile int *>(sm + kOffAgain);
                 if (tx == 0) {
                     // whether X^T's values, the M group's too, are finite and fit kXUnit
-                    any_bad[k & 1] = any_bad[2 + (k & 1)] = 0;
-                    reinterpret_cast<float *>(sm + kOffXMost)[k & 1] = 65504.0f / kXUnit;
-                    ok = wait(true, mb_mc, k & 1);
-                    const bool other = off || *reinterpret_cast<volatile int *>(sm + kOffMOff) != 0 ||
-                                       *reinterpret_cast<volatile int *>(sm + kOffSeen) != k + 1;
+                    const int par = k & 1;
+                    any_bad[par] = any_bad[2 + par] = 0;
+                    ok = wait(true, mb_mc, par);
+                    volatile uint32_t *xh = reinterpret_cast<volatile uint32_t *>(sm + kOffXHead) + 2 * par;
+                    const uint32_t x0 = xh[0], x1 = xh[1];
+                    xh[0] = xh[1] = 0u;
+                    const bool other = off || *reinterpret_cast<volatile int *>(sm + kOffMOff) != 0 || max(x0, x1) < 0x0c00u;   // (2^-12)
+                    float *xm = reinterpret_cast<float *>(sm + kOffXMost) + 2 * par;
+                    xm[0] = other ? 0.0f : __half2float(__ushort_as_half((uint16_t)x0)) * (1.0f / kXUnit);
+                    xm[1] = other ? 0.0f : __half2float(__ushort_as_half((uint16_t)x1)) * (1.0f / kXUnit);
                     if (!other) {
                         tc::mbar_arrive(of(mb_w0, k));
                         tc::mbar_arrive(of(mb_free0, k));

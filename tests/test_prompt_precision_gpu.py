@@ -141,3 +141,29 @@ def test_rows_of_many_growing_chunks(lib):
     for rows in (slice(0, 21000), slice(21000, n)):
         assert ref.far(y[rows], wy[rows]) <= 6e-3
     assert ref.far(s, ws) <= 1e-5
+
+
+@pytest.mark.parametrize("memory", [(1e-3, 1e-2), (0.02, 16.0)])
+def test_channels_far_smaller_than_their_head_s_others(lib, memory):
+    """x of channels 1e-1 to 1e-6 times the others' all along (D = 0, so that y
+    is their states' and the chunk's alone): as exact for their size."""
+    shape, n = (2, 64, 128), 3000
+    H, P, N = shape
+    d = ref.draw(n, 1, *shape, torch.bfloat16, seed=35, pool=1, a_range=memory, bias=False)
+    d["D"] = torch.zeros(H)
+    for c in range(8, P):
+        d["xbc"][:, c] = (d["xbc"][:, c].float() * 10.0 ** -(c // 8 - 1)).to(torch.bfloat16)
+        d["state"][0, 0, c] *= 10.0 ** -(c // 8 - 1)
+        d["tail"][..., c] = (d["tail"][..., c].float() * 10.0 ** -(c // 8 - 1)).to(torch.bfloat16)
+    y, s, _ = ref.run(lib, d, [n], [1], *shape)
+    assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+    wy, ws, _ = ref.prompts(d, [n], [1], *shape)
+    terms, _ = _terms(d, n, shape)
+    # (2-norms of channels: the roundings of B and C in G, 1.7e-3 each of terms that cancel in part; 6e-3)
+    off = np.linalg.norm(to_np(y) - wy, axis=0) / np.linalg.norm(wy, axis=0)
+    assert off.max() <= 6e-3, [float(v) for v in off[::8]]
+    off = np.abs(to_np(y) - wy) - Y_PART * np.abs(wy) - A_PART * terms
+    assert off.max() <= 0
+    # (2-norm: where one token outweighs the others, its conv may cancel, which the
+    # magnitudes of activations do not show)
+    assert ref.far(s, ws) <= 1e-5
