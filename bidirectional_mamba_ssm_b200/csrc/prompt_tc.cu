@@ -1699,7 +1699,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     volatile uint32_t *xh = reinterpret_cast<volatile uint32_t *>(sm + kOffXHead) + 2 * par;
                     const uint32_t x0 = xh[0], x1 = xh[1];
                     xh[0] = xh[1] = 0u;
-                    const bool other = off || *reinterpret_cast<volatile int *>(sm + kOffMOff) != 0 || max(x0, x1) < 0x0c00u;   // (2^-12)
+                    auto small = [](uint32_t x) { return x - 1u < 0x0c00u - 1u; };   // (below 2^-12, not 0)
+                    const bool other = off || *reinterpret_cast<volatile int *>(sm + kOffMOff) != 0 || small(x0) || small(x1);
                     float *xm = reinterpret_cast<float *>(sm + kOffXMost) + 2 * par;
                     xm[0] = other ? 0.0f : __half2float(__ushort_as_half((uint16_t)x0)) * (1.0f / kXUnit);
                     xm[1] = other ? 0.0f : __half2float(__ushort_as_half((uint16_t)x1)) * (1.0f / kXUnit);

@@ -391,9 +391,9 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
  * An infinity or NaN among a prompt's inputs reaches its own rows from that
  * token on (the heads and channels that it enters) and its entry, no others.
  * y is as exact as fp32 sums rounded once to dtype.  (bf16 at headdim 64 and
- * d_state 128: an activation of x below 2^-24, in a chunk of 128 tokens that has
- * larger ones, counts to the nearest 2^-33; one past 2^8 takes its chunk some 2.3
- * times as long.)
+ * d_state 128: an activation of x below 2^-24, beside larger ones of its head
+ * in a chunk of 128 tokens, counts to the nearest 2^-32; one past 2^8, or a head
+ * with none from 2^-20 on, takes its chunk some 2.3 times as long.)
  * y must not overlap an input or the pool.  len up to 2^30 (else
  * BIMAMBA_ERR_UNSUPPORTED).
  */
