@@ -33,8 +33,8 @@
 // below the accumulator's last bit: onto the state itself, thousands of such
 // steps were off by 2e-5 after 32768 tokens).  So no error adds up with the
 // number of chunks.  A value below 2^-29 of its scale keeps fewer than 11 bits:
-// an activation below 2^-24 in a chunk of larger ones, or far below its
-// channel's largest where that is past 2^8.
+// an activation below 2^-24 beside larger ones of its head in a chunk, or far
+// below its channel's largest where that is past 2^8.
 //
 // A token's infinity or NaN must not reach the rows before it, but in M X it
 // meets their zeros (0 inf = NaN): such values enter X as zeros, and the rows
@@ -57,7 +57,7 @@
 // C S^T, 16 M X, 24 state) = 3.6K cycles, about 20K warp instructions (conv
 // and SiLU, operand splitting, M, state and output scaling) = 5K cycles of
 // the four schedulers, and HBM 66 KB = 1.5K cycles at the SM's share.  It
-// takes 8.9K: the chain from one chunk's state product to the next's (copy of
+// takes 9.0K: the chain from one chunk's state product to the next's (copy of
 // the state, C S^T, scaled rows, M X, G), of which the latencies of the
 // products and the hand-offs are half.  Issuing the next state product ahead
 // of G or M X, or freeing (w o X)^T a quarter at a time, gains nothing: the
@@ -66,8 +66,8 @@
 // Measured, 64 heads, calls one after another on the same buffers, three cards:
 // 8 prompts of 4096 tokens 374..386 us, one of 32768 534..552, 11 ragged ones of
 // 8126 in all 136..139, 37 tokens 22.5 (18 of them the host's call).  On one card
-// in turn with the form whose operands were all bf16: 364 for 341, 506 for 504,
-// 137 for 129.
+// in turn with the form whose operands were all bf16: 371 for 338, 515 for 502,
+// 138 for 127.
 #include "common.cuh"
 #include "dispatch.h"
 #include "tc_ptx.cuh"
@@ -899,8 +899,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // from the raw rows: values that are not finite as zeros, the first such
     // token of a channel noted in bad_at; a channel whose largest value is past
     // fp16's range or near its small end times a power of two of its own.  (8
-    // prompts of 4096 tokens whose every chunk has activations past 2^8: 835 us
-    // for 375.)
+    // prompts of 4096 tokens whose every chunk has activations past 2^8: 828 us
+    // for 380.)
     float *xfac = reinterpret_cast<float *>(sm + kOffXFac);
     auto repair = [&](int k, int third, int pr) {
         const int par = k & 1;
@@ -1467,7 +1467,8 @@ prompt_walk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // the fp16 copy of the state (operand of C S^T), times a power of two
         // whose inverse C S^T is multiplied by: one for the head, and for rows
         // whose largest value is below 2^-16 of its (or above 2^60) their own, which
-        // (rare) takes another pass over C S^T's columns
+        // (rare) takes another pass over C S^T's columns (8 prompts of 4096 tokens,
+        // such rows in every head and chunk: 464 us for 380)
         float *colf = reinterpret_cast<float *>(sm + kOffColF), *headf = reinterpret_cast<float *>(sm + kOffHeadF);
         int *rowwise = reinterpret_cast<int *>(sm + kOffRowwise);   // [head]: last chunk + 1 with such rows
         float copy_scale = 1.0f;
