@@ -34,7 +34,9 @@
 // steps were off by 2e-5 after 32768 tokens).  So no error adds up with the
 // number of chunks.  A value below 2^-29 of its scale keeps fewer than 11 bits:
 // an activation below 2^-24 beside larger ones of its head in a chunk, or far
-// below its channel's largest where that is past 2^8.
+// below its channel's largest where that is past 2^8.  The conv makes X times
+// kXUnit (the state's weights are divided by it), so that a sum from 2^120 on is
+// an infinity: the unit after it would be one more product a value.
 //
 // A token's infinity or NaN must not reach the rows before it, but in M X it
 // meets their zeros (0 inf = NaN): such values enter X as zeros, and the rows

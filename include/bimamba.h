@@ -392,8 +392,10 @@ int bimamba_block_decode_pool(const bimamba_dims *d, const void *xbc_block,
  * token on (the heads and channels that it enters) and its entry, no others.
  * y is as exact as fp32 sums rounded once to dtype.  (bf16 at headdim 64 and
  * d_state 128: an activation of x below 2^-24, beside larger ones of its head
- * in a chunk of 128 tokens, counts to the nearest 2^-32; one past 2^8, or a head
- * with none from 2^-20 on, takes its chunk some 2.3 times as long.)
+ * in a chunk of 128 tokens, counts to the nearest 2^-32, and a token of the chunk
+ * whose dt B is below 2^-29 of the largest that reaches a row, or of |D|, with
+ * fewer bits; an activation past 2^8, or a head with none from 2^-20 on, takes its
+ * chunk some 2.3 times as long; a conv sum of 2^120 or more counts as an infinity.)
  * y must not overlap an input or the pool.  len up to 2^30 (else
  * BIMAMBA_ERR_UNSUPPORTED).
  */

@@ -168,3 +168,28 @@ def test_channels_far_smaller_than_their_head_s_others(lib, memory):
     # (2-norm: where one token outweighs the others, its conv may cancel, which the
     # magnitudes of activations do not show)
     assert ref.far(s, ws) <= 1e-5
+
+
+def test_a_sum_past_the_range_is_an_infinity(lib):
+    """Raw values whose conv sum is past 2^120 (here above 2^128 / 16 in
+    magnitude) act as infinities do: on their channel from their token on."""
+    shape, n = (2, 64, 128), 300
+    d = ref.draw(n, 1, *shape, torch.bfloat16, seed=36, pool=1)
+    d["conv_w"][70] = torch.tensor([0.25, 0.5, 0.125, 0.25])
+    outs = []
+    for v in (3e38, float("inf")):
+        big = dict(d, xbc=d["xbc"].clone())
+        big["xbc"][140, 70] = v
+        outs.append(ref.run(lib, big, [n], [1], *shape))
+        assert lib.bimamba_get_error() == lib.BIMAMBA_OK
+    y0, s0, _ = ref.run(lib, d, [n], [1], *shape)
+    for a, b in zip(outs[0][:2], outs[1][:2]):
+        assert torch.equal(a.isnan(), b.isnan())
+        assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+    y, s = outs[0][:2]
+    rest = [c for c in range(128) if c != 70]
+    assert torch.equal(y[:140], y0[:140])
+    assert torch.equal(y[:, rest], y0[:, rest])
+    assert not y[140:, 70].isfinite().any() and not s[0, 1, 6].isfinite().any()
+    keep = [c for c in range(64) if c != 6]
+    assert torch.equal(s[0, 0], s0[0, 0]) and torch.equal(s[0, 1, keep], s0[0, 1, keep])
